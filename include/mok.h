@@ -344,6 +344,161 @@ mok_status mok_route_backward(const int32_t *topk_ids, const float *topk_w, cons
                               int64_t T, int32_t E, int32_t k, float *dlogits, void *stream);
 
 /*
+ * Operators around the routed experts in a transformer block. The pages
+ * describe the routed layer alone; these take the plainest readings: dropout of
+ * a branch, the residual's addition with a root-mean-square norm, and the
+ * dense gated feed-forward block (a shared expert).
+ *
+ * Conventions beside the ones at the top of this file:
+ *  - The residual stream (residual, sum, their gradients) is bf16 or fp32:
+ *    stream_dtype. Branches, normalised rows and weights are bf16.
+ *  - Dropout masks come from a counter-based generator and are never stored.
+ *    rng points to two device uint64, {seed, offset}; element i of a call is
+ *    word i % 4 of the Philox4x32-10 block with key seed and 64-bit counter
+ *    offset + i / 4 (the counter's upper 64 bits are 0), and is kept when the
+ *    word is at least floor(p * 2^32). A kept value is multiplied by the fp32
+ *    value of 1 / (1 - p); a dropped one contributes nothing, whatever it
+ *    holds. A call of n elements uses (n + 3) / 4 counters; the caller advances
+ *    offset by at least that much before the next draw, and keeps the old pair
+ *    for the backward. Both are read when the call's kernels run, so replays of
+ *    a captured graph follow the pair's current value. With p == 0 rng is
+ *    ignored and may be NULL.
+ *  - An output may be the same buffer as an input of the same type and shape
+ *    only where a call says so; otherwise buffers must not overlap.
+ */
+#define MOK_STREAM_BF16 0
+#define MOK_STREAM_F32 1
+
+/*
+ * out = residual + dropout(x).
+ *   x         device bf16 [n], any n in [0, 2^40)
+ *   residual  device stream_dtype [n], or NULL (then out = dropout(x))
+ *   p         drop probability in [0, 1)
+ *   out       device stream_dtype [n]; may be residual's buffer, or x's when
+ *             the stream is bf16
+ */
+mok_status mok_dropout(const void *x, const void *residual, int64_t n, float p, const uint64_t *rng,
+                       int32_t stream_dtype, void *out, void *stream);
+
+/*
+ * Gradient of mok_dropout with respect to x: dx = dy / (1 - p) where the
+ * forward kept the element, 0 elsewhere. (The residual's gradient is dy.)
+ *   dy  device stream_dtype [n];  dx  device bf16 [n], may be dy's buffer when
+ *   the stream is bf16. p and rng as the forward had them.
+ */
+mok_status mok_dropout_backward(const void *dy, int64_t n, float p, const uint64_t *rng, int32_t stream_dtype,
+                                void *dx, void *stream);
+
+/*
+ * Residual addition and root-mean-square norm. T >= 0 rows (below 2^31) of H
+ * elements, H a multiple of 8 (of 32 for MXFP8 rows) up to 16384; eps >= 0.
+ */
+typedef struct mok_norm_shape {
+    int64_t T;
+    int32_t H;
+    int32_t stream_dtype;
+    float eps;
+    float p;   /* drop probability of the branch, in [0, 1) */
+} mok_norm_shape;
+
+/*
+ * s = residual + dropout(x) in fp32 (element i of the dropout is t * H + h),
+ * rstd = 1 / sqrt(mean over h of s^2 + eps), y = s * rstd * weight. Statistics
+ * and y come from the fp32 s; sum is its copy in the stream's type.
+ *   x         device bf16 [T,H], the branch
+ *   residual  device stream_dtype [T,H], or NULL (then s = dropout(x))
+ *   weight    device bf16 [H]
+ *   sum       device stream_dtype [T,H], or NULL; may be residual's buffer, or
+ *             x's when the stream is bf16
+ *   y         device bf16 [T,H], or NULL
+ *   y_elems, y_scales   y as MXFP8 (mok_mxfp8_quantize's block format along H,
+ *             rounded from the fp32 y): device uint8 [T,H] and [T,H/32], or
+ *             both NULL. At least one of y and y_elems is given.
+ *   rstd      device fp32 [T]
+ * s^2 must not overflow fp32 (|s| up to about 10^17).
+ */
+mok_status mok_add_rmsnorm(const mok_norm_shape *shape, const void *x, const void *residual, const void *weight,
+                           const uint64_t *rng, void *sum, void *y, uint8_t *y_elems, uint8_t *y_scales,
+                           float *rstd, void *stream);
+
+/* Host-only: workspace bytes of mok_add_rmsnorm_backward for shape (a
+   workspace for T rows also serves fewer). */
+mok_status mok_add_rmsnorm_backward_size(const mok_norm_shape *shape, size_t *workspace_bytes);
+
+/*
+ * Backward of mok_add_rmsnorm from its sum and rstd:
+ *   ds = dsum + rstd * (dy * weight - sum * rstd^2 * mean over h of dy * weight * sum)
+ *   dy         device bf16 [T,H], gradient of y
+ *   sum, rstd  as the forward wrote them
+ *   dsum       device stream_dtype [T,H], the gradient that reaches s along
+ *              the residual stream, or NULL (zero)
+ *   dresidual  device stream_dtype [T,H]: ds; or NULL. May be dsum's buffer.
+ *   dx         device bf16 [T,H]: the branch's gradient, ds through the
+ *              dropout; or NULL. May be dy's buffer.
+ *   dweight    device fp32 [H]: sum over t of dy * sum * rstd (zeros for T == 0)
+ *   workspace  at least mok_add_rmsnorm_backward_size bytes
+ * p, eps and rng as the forward had them. Bitwise deterministic.
+ */
+mok_status mok_add_rmsnorm_backward(const mok_norm_shape *shape, void *workspace, size_t workspace_bytes,
+                                    const void *dy, const void *sum, const void *weight, const float *rstd,
+                                    const void *dsum, const uint64_t *rng, void *dresidual, void *dx,
+                                    float *dweight, void *stream);
+
+/*
+ * Dense gated feed-forward block (SwiGLU), the shared expert beside the routed
+ * ones: T rows of H through an intermediate size I.
+ * H and I are multiples of 64 (128 in MXFP8); T >= 0; the layer's bounds on
+ * byte offsets hold: T*H*2 < 2^31, T*I*4 < 2^31, (H+256)*I*2 < 2^31 and
+ * (I+256)*H*2 < 2^31.
+ * precision is MOK_BF16 or MOK_MXFP8 (weight gradients in BF16).
+ * Weights are a mok_weights for one expert (E = 1), in the orientations that
+ * struct describes.
+ */
+typedef struct mok_ffn_shape {
+    int64_t T;
+    int32_t H, I;
+    int32_t precision;
+} mok_ffn_shape;
+
+/* Host-only: workspace bytes that mok_ffn_forward and mok_ffn_backward need (a
+   workspace for T rows also serves fewer). */
+mok_status mok_ffn_query_size(const mok_ffn_shape *shape, size_t *workspace_bytes);
+
+/*
+ * out = addend + (silu(x W_gate) * (x W_up)) W_down.
+ *   x         BF16: device bf16 [T,H]. MXFP8: NULL
+ *   x_elems, x_scales   MXFP8: device uint8 [T,H], [T,H/32], the rows quantized
+ *             along H (mok_add_rmsnorm or mok_mxfp8_quantize). BF16: NULL
+ *   addend    device bf16 [T,H] added to the block's output in fp32 (for
+ *             instance mok_forward's out), or NULL
+ *   out       device bf16 [T,H]; may be addend's buffer
+ *   h         device bf16 [T,2I]: x [W_gate | W_up], which the backward needs,
+ *             or NULL
+ * Bitwise deterministic.
+ */
+mok_status mok_ffn_forward(const mok_ffn_shape *shape, void *workspace, size_t workspace_bytes, const void *x,
+                           const uint8_t *x_elems, const uint8_t *x_scales, const mok_weights *w,
+                           const void *addend, void *out, void *h, void *stream);
+
+/*
+ * Backward of mok_ffn_forward for the gradient dy of out.
+ *   x         device bf16 [T,H] in either precision (the weight gradients'
+ *             operand)
+ *   w         the weights; MXFP8: in the backward's orientation
+ *   h         device bf16 [T,2I], as the forward wrote it
+ *   dy        device bf16 [T,H]
+ *   addend    device bf16 [T,H] added to dx in fp32 (for instance mok_backward's
+ *             dx), or NULL
+ *   dx        device bf16 [T,H]; may be addend's buffer
+ *   dw_gate, dw_up [H,I] and dw_down [I,H], device bf16, overwritten (zeros
+ *             for T == 0)
+ * Bitwise deterministic.
+ */
+mok_status mok_ffn_backward(const mok_ffn_shape *shape, void *workspace, size_t workspace_bytes, const void *x,
+                            const mok_weights *w, const void *h, const void *dy, const void *addend, void *dx,
+                            void *dw_gate, void *dw_up, void *dw_down, void *stream);
+
+/*
  * Measurement aid, not part of the layer: per-kernel durations for tools such
  * as benchmarks. While enabled, every kernel launch of the library is
  * bracketed by two HIP events recorded on the launch's own stream (the

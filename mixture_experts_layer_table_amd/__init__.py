@@ -12,7 +12,8 @@ project summary, Functional API and Key-concepts table):
   tensors are passed as raw pointers and the caller owns every buffer.
 * ``MoKConfig``, ``get_workspace``, ``build_schedule``, ``forward``,
   ``backward``, ``mxfp8_quantize`` — allocate the caller-side buffers with
-  torch and call the entry points above.
+  torch and call the entry points above. Around the layer: ``dropout``,
+  ``add_rmsnorm``, ``get_ffn_workspace``, ``ffn_forward`` and their backwards.
 """
 from __future__ import annotations
 
@@ -42,10 +43,13 @@ MOK_DEBUG_IDENTITY_EXPERT, MOK_DEBUG_SEPARATE_LAUNCHES, MOK_DEBUG_WHOLE_PASS, MO
 EXPORTS = ("mok_config_default", "mok_config_autosize", "mok_query_sizes", "mok_schedule_layout_query",
            "mok_build_schedule", "mok_forward", "mok_backward", "mok_mxfp8_quantize", "mok_route",
            "mok_route_backward", "mok_status_string", "mok_kernel_timing_enable", "mok_kernel_timing_read",
-           "mok_last_error", "mok_forward_noalloc", "mok_item_trace_enable", "mok_item_trace_read")
+           "mok_last_error", "mok_forward_noalloc", "mok_item_trace_enable", "mok_item_trace_read",
+           "mok_dropout", "mok_dropout_backward", "mok_add_rmsnorm", "mok_add_rmsnorm_backward_size",
+           "mok_add_rmsnorm_backward", "mok_ffn_query_size", "mok_ffn_forward", "mok_ffn_backward")
 MOK_TRACE_FWD_GEMMS, MOK_TRACE_BWD_GEMMS, MOK_TRACE_WGRAD_GATE_UP, MOK_TRACE_WGRAD_DOWN, MOK_TRACE_OTHER = range(5)
 MOK_ITEM_TRACE_CAPACITY = 65536
 MOK_NOALLOC_SCRATCH_BYTES = 64 << 20
+MOK_STREAM_BF16, MOK_STREAM_F32 = 0, 1
 
 
 class mok_config(ctypes.Structure):
@@ -65,6 +69,16 @@ class mok_weights(ctypes.Structure):
                 ("gate_elems", ctypes.c_void_p), ("gate_scales", ctypes.c_void_p),
                 ("up_elems", ctypes.c_void_p), ("up_scales", ctypes.c_void_p),
                 ("down_elems", ctypes.c_void_p), ("down_scales", ctypes.c_void_p)]
+
+
+class mok_norm_shape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int32), ("stream_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("p", ctypes.c_float)]
+
+
+class mok_ffn_shape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int32), ("I", ctypes.c_int32),
+                ("precision", ctypes.c_int32)]
 
 
 class mok_kernel_stat(ctypes.Structure):
@@ -107,6 +121,17 @@ _sigs = {
                            _P, _P, _P],
     "mok_route": [_P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _P, _P, _P],
     "mok_route_backward": [_P, _P, _P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _P, _P],
+    "mok_dropout": [_P, _P, ctypes.c_int64, ctypes.c_float, _P, ctypes.c_int32, _P, _P],
+    "mok_dropout_backward": [_P, ctypes.c_int64, ctypes.c_float, _P, ctypes.c_int32, _P, _P],
+    "mok_add_rmsnorm": [ctypes.POINTER(mok_norm_shape), _P, _P, _P, _P, _P, _P, _P, _P, _P, _P],
+    "mok_add_rmsnorm_backward_size": [ctypes.POINTER(mok_norm_shape), _sz],
+    "mok_add_rmsnorm_backward": [ctypes.POINTER(mok_norm_shape), _P, ctypes.c_size_t, _P, _P, _P, _P, _P, _P, _P,
+                                 _P, _P, _P],
+    "mok_ffn_query_size": [ctypes.POINTER(mok_ffn_shape), _sz],
+    "mok_ffn_forward": [ctypes.POINTER(mok_ffn_shape), _P, ctypes.c_size_t, _P, _P, _P,
+                        ctypes.POINTER(mok_weights), _P, _P, _P, _P],
+    "mok_ffn_backward": [ctypes.POINTER(mok_ffn_shape), _P, ctypes.c_size_t, _P, ctypes.POINTER(mok_weights), _P, _P,
+                         _P, _P, _P, _P, _P, _P],
     "mok_kernel_timing_enable": [ctypes.c_int32],
     "mok_item_trace_enable": [ctypes.c_int32],
     "mok_item_trace_read": [ctypes.POINTER(mok_item_record), ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)],
@@ -195,6 +220,43 @@ def mok_route(logits, T, E, k, topk_ids, topk_w, stream):
 
 def mok_route_backward(topk_ids, topk_w, dtopk_w, T, E, k, dlogits, stream):
     return _lib.mok_route_backward(topk_ids, topk_w, dtopk_w, T, E, k, dlogits, stream)
+
+
+def mok_dropout(x, residual, n, p, rng, stream_dtype, out, stream):
+    return _lib.mok_dropout(x, residual, n, p, rng, stream_dtype, out, stream)
+
+
+def mok_dropout_backward(dy, n, p, rng, stream_dtype, dx, stream):
+    return _lib.mok_dropout_backward(dy, n, p, rng, stream_dtype, dx, stream)
+
+
+def mok_add_rmsnorm(shape, x, residual, weight, rng, sum, y, y_elems, y_scales, rstd, stream):
+    return _lib.mok_add_rmsnorm(ctypes.byref(shape), x, residual, weight, rng, sum, y, y_elems, y_scales, rstd, stream)
+
+
+def mok_add_rmsnorm_backward_size(shape, workspace):
+    return _lib.mok_add_rmsnorm_backward_size(ctypes.byref(shape), workspace)
+
+
+def mok_add_rmsnorm_backward(shape, workspace, workspace_bytes, dy, sum, weight, rstd, dsum, rng, dresidual, dx,
+                             dweight, stream):
+    return _lib.mok_add_rmsnorm_backward(ctypes.byref(shape), workspace, workspace_bytes, dy, sum, weight, rstd, dsum,
+                                         rng, dresidual, dx, dweight, stream)
+
+
+def mok_ffn_query_size(shape, workspace):
+    return _lib.mok_ffn_query_size(ctypes.byref(shape), workspace)
+
+
+def mok_ffn_forward(shape, workspace, workspace_bytes, x, x_elems, x_scales, weights, addend, out, h, stream):
+    return _lib.mok_ffn_forward(ctypes.byref(shape), workspace, workspace_bytes, x, x_elems, x_scales,
+                                ctypes.byref(weights), addend, out, h, stream)
+
+
+def mok_ffn_backward(shape, workspace, workspace_bytes, x, weights, h, dy, addend, dx, dw_gate, dw_up, dw_down,
+                     stream):
+    return _lib.mok_ffn_backward(ctypes.byref(shape), workspace, workspace_bytes, x, ctypes.byref(weights), h, dy,
+                                 addend, dx, dw_gate, dw_up, dw_down, stream)
 
 
 def mok_kernel_timing_enable(enable):
@@ -525,6 +587,276 @@ def route_backward(topk_ids, topk_w, dtopk_w, E: int):
     _check(mok_route_backward(_ptr(topk_ids), _ptr(topk_w), _ptr(dtopk_w), T, E, k, _ptr(dl), _stream()),
            "mok_route_backward")
     return dl
+
+
+# ----------------------------------------------------------------------------- around the routed experts
+
+_STREAM_DTYPES = {torch.bfloat16: MOK_STREAM_BF16, torch.float32: MOK_STREAM_F32}
+
+
+def _on_device(t):
+    """(current stream of t's device, guard that makes that device current): the
+    kernels go to the device that holds the tensors, whatever device is current."""
+    if t.device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, got {t.device}")
+    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream), torch.cuda.device(t.device)
+
+
+def _stream_dtype(dtype, name):
+    if dtype not in _STREAM_DTYPES:
+        raise ValueError(f"{name}: dtype {dtype}, expected torch.bfloat16 or torch.float32")
+    return _STREAM_DTYPES[dtype]
+
+
+def _check_rng(p, rng, device):
+    """rng: int64 [2] on the device, {seed, offset} as bit patterns; unused when p == 0."""
+    if not 0.0 <= p < 1.0:
+        raise ValueError(f"p: {p}, expected a value in [0, 1)")
+    if p > 0.0:
+        _require(rng, "rng", torch.int64, (2,), device)
+
+
+def dropout(x, rng, p: float, residual=None, out=None):
+    """residual + dropout(x) (mok_dropout). x: bf16, any shape; residual: bf16 or
+    fp32 of that shape, or None; rng: int64 [2] on the device, {seed, offset}.
+    Returns a tensor of residual's type (bf16 without one); ``out`` may be
+    residual. A call draws (x.numel() + 3) // 4 counters from offset on."""
+    shape, dev = tuple(x.shape), x.device
+    _require(x, "x", torch.bfloat16, shape)
+    dtype = torch.bfloat16 if residual is None else residual.dtype
+    sd = _stream_dtype(dtype, "residual")
+    if residual is not None:
+        _require(residual, "residual", dtype, shape, dev)
+    _check_rng(p, rng, dev)
+    st, guard = _on_device(x)
+    with guard:
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=dev)
+        else:
+            _require(out, "out", dtype, shape, dev)
+        _check(mok_dropout(_ptr(x), _ptr(residual), x.numel(), p, _ptr(rng), sd, _ptr(out), st), "mok_dropout")
+    return out
+
+
+def dropout_backward(dy, rng, p: float, dx=None):
+    """Gradient of dropout() with respect to x, bf16 (mok_dropout_backward); p and
+    rng as the forward had them. The residual's gradient is dy itself."""
+    shape, dev = tuple(dy.shape), dy.device
+    sd = _stream_dtype(dy.dtype, "dy")
+    _require(dy, "dy", dy.dtype, shape)
+    _check_rng(p, rng, dev)
+    st, guard = _on_device(dy)
+    with guard:
+        if dx is None:
+            dx = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        else:
+            _require(dx, "dx", torch.bfloat16, shape, dev)
+        _check(mok_dropout_backward(_ptr(dy), dy.numel(), p, _ptr(rng), sd, _ptr(dx), st), "mok_dropout_backward")
+    return dx
+
+
+def add_rmsnorm(x, weight, eps: float, residual=None, p: float = 0.0, rng=None, stream_dtype=None, y: bool = True,
+                mxfp8: bool = False, outs=None):
+    """Residual addition (with dropout of x) and RMS norm (mok_add_rmsnorm).
+    x: bf16 [T, H]; weight: bf16 [H]; residual: [T, H] in the stream's type or
+    None. stream_dtype defaults to residual's type (bf16 without one). Returns a
+    dict: sum [T, H] in the stream's type, rstd fp32 [T], y bf16 [T, H] (if
+    ``y``), y_elems uint8 [T, H] and y_scales uint8 [T, H/32] (if ``mxfp8``).
+    ``outs``: the same keys, caller-given; sum may be residual."""
+    if x.dim() != 2:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected [T, H]")
+    T, H = x.shape
+    dev = x.device
+    dtype = stream_dtype or (torch.bfloat16 if residual is None else residual.dtype)
+    sd = _stream_dtype(dtype, "stream_dtype")
+    _require(x, "x", torch.bfloat16, (T, H))
+    _require(weight, "weight", torch.bfloat16, (H,), dev)
+    if residual is not None:
+        _require(residual, "residual", dtype, (T, H), dev)
+    _check_rng(p, rng, dev)
+    shapes = dict(sum=((T, H), dtype), rstd=((T,), torch.float32))
+    if y:
+        shapes["y"] = ((T, H), torch.bfloat16)
+    if mxfp8:
+        if H % 32:
+            raise ValueError(f"x: H = {H}, MXFP8 rows need a multiple of 32")
+        shapes["y_elems"], shapes["y_scales"] = ((T, H), torch.uint8), ((T, H // 32), torch.uint8)
+    st, guard = _on_device(x)
+    with guard:
+        if outs is None:
+            outs = {n: torch.empty(sh, dtype=dt, device=dev) for n, (sh, dt) in shapes.items()}
+        else:
+            for n, (sh, dt) in shapes.items():
+                _require(outs.get(n), n, dt, sh, dev)
+            outs = {n: outs[n] for n in shapes}
+        _check(mok_add_rmsnorm(mok_norm_shape(T, H, sd, eps, p), _ptr(x), _ptr(residual), _ptr(weight), _ptr(rng),
+                               _ptr(outs["sum"]), _ptr(outs.get("y")), _ptr(outs.get("y_elems")),
+                               _ptr(outs.get("y_scales")), _ptr(outs["rstd"]), st), "mok_add_rmsnorm")
+    return outs
+
+
+def add_rmsnorm_backward(dy, sum, weight, rstd, dsum=None, p: float = 0.0, rng=None, grads=None, workspace=None):
+    """Backward of add_rmsnorm() from its sum and rstd (mok_add_rmsnorm_backward).
+    dy: bf16 [T, H]; dsum: [T, H] in sum's type, the gradient along the residual
+    stream, or None. Returns a dict: dresidual [T, H] in sum's type, dx bf16
+    [T, H] (the same tensor as dresidual where both are bf16 and p == 0),
+    dweight fp32 [H]. ``workspace``: uint8, made here if None."""
+    if sum.dim() != 2:
+        raise ValueError(f"sum: shape {tuple(sum.shape)}, expected [T, H]")
+    T, H = sum.shape
+    dev, dtype = sum.device, sum.dtype
+    sd = _stream_dtype(dtype, "sum")
+    _require(sum, "sum", dtype, (T, H))
+    _require(dy, "dy", torch.bfloat16, (T, H), dev)
+    _require(weight, "weight", torch.bfloat16, (H,), dev)
+    _require(rstd, "rstd", torch.float32, (T,), dev)
+    if dsum is not None:
+        _require(dsum, "dsum", dtype, (T, H), dev)
+    _check_rng(p, rng, dev)
+    shape = mok_norm_shape(T, H, sd, 0.0, p)
+    need = ctypes.c_size_t()
+    _check(mok_add_rmsnorm_backward_size(shape, ctypes.byref(need)), "mok_add_rmsnorm_backward_size")
+    separate = p > 0.0 or dtype != torch.bfloat16
+    shapes = dict(dresidual=((T, H), dtype), dweight=((H,), torch.float32))
+    if separate:
+        shapes["dx"] = ((T, H), torch.bfloat16)
+    st, guard = _on_device(sum)
+    with guard:
+        if workspace is None:
+            workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
+        _require_bytes(workspace, "workspace", need.value, dev)
+        if grads is None:
+            grads = {n: torch.empty(sh, dtype=dt, device=dev) for n, (sh, dt) in shapes.items()}
+        else:
+            for n, (sh, dt) in shapes.items():
+                _require(grads.get(n), n, dt, sh, dev)
+            grads = {n: grads[n] for n in shapes}
+        _check(mok_add_rmsnorm_backward(shape, _ptr(workspace), workspace.numel(), _ptr(dy), _ptr(sum), _ptr(weight),
+                                        _ptr(rstd), _ptr(dsum), _ptr(rng), _ptr(grads["dresidual"]),
+                                        _ptr(grads.get("dx")), _ptr(grads["dweight"]), st),
+               "mok_add_rmsnorm_backward")
+    if not separate:
+        grads["dx"] = grads["dresidual"]
+    return grads
+
+
+@dataclasses.dataclass
+class FfnWorkspace:
+    """Caller-owned scratch of the feed-forward block for up to T rows (made once, reused)."""
+    precision: int
+    T: int
+    H: int
+    I: int
+    buffer: "object"        # torch.uint8 tensor
+
+
+def get_ffn_workspace(precision: int = MOK_BF16, *, device, num_tokens: int, hidden_size: int,
+                      intermediate_size: int) -> FfnWorkspace:
+    need = ctypes.c_size_t()
+    _check(mok_ffn_query_size(mok_ffn_shape(num_tokens, hidden_size, intermediate_size, precision),
+                              ctypes.byref(need)), "mok_ffn_query_size")
+    buf = torch.empty(need.value, dtype=torch.uint8, device=device)
+    return FfnWorkspace(precision, num_tokens, hidden_size, intermediate_size, buf)
+
+
+def _check_ffn_weights(ws: FfnWorkspace, weights: mok_weights, orientation: str):
+    """Shapes, dtypes and devices of the tensors a weight struct refers to: one
+    expert's, with or without a leading dimension of 1."""
+    tensors = getattr(weights, "_tensors", None)
+    if tensors is None:          # a hand-made struct: nothing to check against
+        return
+    dev, H, I = ws.buffer.device, ws.H, ws.I
+    kind = getattr(weights, "_kind", "")
+
+    def one(t, name, dtype, shape):
+        _require(t, name, dtype, (1,) + shape if isinstance(t, torch.Tensor) and t.dim() == 3 else shape, dev)
+
+    if ws.precision == MOK_BF16:
+        if not kind.startswith("bf16"):
+            raise ValueError("BF16 mode needs bf16 weights (weights_bf16)")
+        for t, n, sh in zip(tensors, ("w_gate", "w_up", "w_down"), ((H, I), (H, I), (I, H))):
+            one(t, n, torch.bfloat16, sh)
+        return
+    if not kind.startswith("mxfp8"):
+        raise ValueError("MXFP8 mode needs quantized weights (MXFP8Weights)")
+    if ":" in kind and kind.split(":")[1] != orientation:
+        raise ValueError(f"MXFP8 weights quantized for {kind.split(':')[1]}, used in {orientation}")
+    shapes = ((I, H), (I, H), (H, I)) if orientation == "fwd" else ((H, I), (H, I), (I, H))
+    for (el, sc), n, sh in zip(tensors, ("gate", "up", "down"), shapes):
+        one(el, n + " elements", torch.uint8, sh)
+        one(sc, n + " scales", torch.uint8, (sh[0], sh[1] // 32))
+
+
+def _ffn_rows(ws: FfnWorkspace, t, name):
+    if t.dim() != 2 or t.shape[0] > ws.T:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [T, {ws.H}] with T <= {ws.T}")
+    return t.shape[0]
+
+
+def ffn_forward(ws: FfnWorkspace, x, weights: mok_weights, addend=None, out=None, h=None, save_h: bool = True):
+    """Dense gated feed-forward block (mok_ffn_forward): out = addend +
+    (silu(x W_gate) * (x W_up)) W_down. x: bf16 [T, H] (T up to ws.T), or in
+    MXFP8 the pair (elems uint8 [T, H], scales uint8 [T, H/32]) that
+    add_rmsnorm(mxfp8=True) or mxfp8_quantize gives. addend: bf16 [T, H] or None;
+    ``out`` may be addend. Returns (out bf16 [T, H], h bf16 [T, 2I] for the
+    backward, or None with save_h=False)."""
+    dev, H, I = ws.buffer.device, ws.H, ws.I
+    elems = scales = rows = None
+    if ws.precision == MOK_BF16:
+        T = _ffn_rows(ws, x, "x")
+        _require(x, "x", torch.bfloat16, (T, H), dev)
+        rows = x
+    else:
+        if not isinstance(x, (tuple, list)) or len(x) != 2:
+            raise ValueError("x: MXFP8 mode takes (elems, scales)")
+        elems, scales = x
+        T = _ffn_rows(ws, elems, "x elements")
+        _require(elems, "x elements", torch.uint8, (T, H), dev)
+        _require(scales, "x scales", torch.uint8, (T, H // 32), dev)
+    _check_ffn_weights(ws, weights, "fwd")
+    if addend is not None:
+        _require(addend, "addend", torch.bfloat16, (T, H), dev)
+    st, guard = _on_device(ws.buffer)
+    with guard:
+        if out is None:
+            out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        else:
+            _require(out, "out", torch.bfloat16, (T, H), dev)
+        if h is not None:
+            _require(h, "h", torch.bfloat16, (T, 2 * I), dev)
+        elif save_h:
+            h = torch.empty((T, 2 * I), dtype=torch.bfloat16, device=dev)
+        _check(mok_ffn_forward(mok_ffn_shape(T, H, I, ws.precision), _ptr(ws.buffer), ws.buffer.numel(), _ptr(rows),
+                               _ptr(elems), _ptr(scales), weights, _ptr(addend), _ptr(out), _ptr(h), st),
+               "mok_ffn_forward")
+    return out, h
+
+
+def ffn_backward(ws: FfnWorkspace, x, weights: mok_weights, h, dy, addend=None, grads=None):
+    """Backward of ffn_forward() (mok_ffn_backward). x: bf16 [T, H] in either
+    precision; weights: in MXFP8 the backward's orientation; addend: bf16 [T, H]
+    added to dx, or None. Returns dict(dx, dw_gate, dw_up, dw_down), bf16;
+    ``grads``: the same keys, caller-given (dx may be addend)."""
+    dev, H, I = ws.buffer.device, ws.H, ws.I
+    T = _ffn_rows(ws, x, "x")
+    _require(x, "x", torch.bfloat16, (T, H), dev)
+    _require(h, "h", torch.bfloat16, (T, 2 * I), dev)
+    _require(dy, "dy", torch.bfloat16, (T, H), dev)
+    if addend is not None:
+        _require(addend, "addend", torch.bfloat16, (T, H), dev)
+    _check_ffn_weights(ws, weights, "bwd")
+    shapes = dict(dx=(T, H), dw_gate=(H, I), dw_up=(H, I), dw_down=(I, H))
+    st, guard = _on_device(ws.buffer)
+    with guard:
+        if grads is None:
+            grads = {n: torch.empty(sh, dtype=torch.bfloat16, device=dev) for n, sh in shapes.items()}
+        else:
+            for n, sh in shapes.items():
+                _require(grads.get(n), n, torch.bfloat16, sh, dev)
+        _check(mok_ffn_backward(mok_ffn_shape(T, H, I, ws.precision), _ptr(ws.buffer), ws.buffer.numel(), _ptr(x),
+                                weights, _ptr(h), _ptr(dy), _ptr(addend), _ptr(grads["dx"]), _ptr(grads["dw_gate"]),
+                                _ptr(grads["dw_up"]), _ptr(grads["dw_down"]), st), "mok_ffn_backward")
+    return grads
 
 
 def read_schedule(schedule, layout: mok_schedule_layout, E: int):

@@ -1,0 +1,395 @@
+// Gated feed-forward block in MXFP8: the four products with a weight operand
+// run on the block-scaled MFMA (gemm8.h), every operand quantized along its
+// contraction axis, 32 values per E8M0 scale:
+//   gate/up  x (given quantized) x W_gate^T | W_up^T
+//   down     a (quantized from its fp32 value in the gate/up epilogue) x W_down^T
+//   dA       dy (quantized here) x W_down
+//   dX       dh (quantized from its fp32 value in the dA epilogue) x W_gate | W_up
+// h, the outputs and the weight gradients are BF16, as in ffn.hip, whose
+// formulas and split over the contraction axis this file shares.
+#include "ffn_parts.h"
+#include "gemm8.h"
+#include "kernels.h"
+#include "mx_block.h"
+
+namespace mok {
+namespace {
+
+using CfgA = TileCfg<256, 256, 2, 4, 4>;
+using CfgS = TileCfg<128, 256, 2, 4, 6>;
+using S8 = Fp8Stage<CfgA>;
+
+__device__ __forceinline__ const uint16_t *as_pairs(const uint8_t *p) { return reinterpret_cast<const uint16_t *>(p); }
+
+struct Ffn8Args {
+    int T, H, I, n_tiles, splits, len;
+    const uint8_t *x, *xs;                // the product's row operand and its scales
+    const uint8_t *w0, *w0s, *w1, *w1s;   // its weights (w1: W_up where both are needed)
+    const uint16_t *addend, *h_in;
+    uint16_t *out, *h, *a, *dh;
+    uint8_t *q, *qs;                      // what the epilogue quantizes: a, or dh
+    float *part;
+};
+
+// Members that every problem below shares: loaders, tile and K-step issue.
+struct Ffn8Base {
+    using C = CfgA;
+    using Args = Ffn8Args;
+    RowLoader<C, C::BM> xl;
+    RowLoader<C, C::BN> wl;
+    ScaleLoader<C> sl;
+    static constexpr int LOADS_PER_STAGE = RowLoader<C, C::BM>::IPW + RowLoader<C, C::BN>::IPW;
+    FfnTile t;
+    int nk;
+    Args a;
+
+    // false: no tile; k0: the run's first value of a contraction axis of K values
+    __device__ bool begin(const Args &args, int b, int K, int &k0) {
+        a = args;
+        if (!ffn_tile(a.T, C::BM, a.n_tiles, a.splits, b, t)) return false;
+        k0 = t.s * a.len * S8::BK8;
+        nk = min(a.len, K / S8::BK8 - t.s * a.len);
+        xl.init(as_pairs(a.x + (int64_t)t.m0 * K + k0), K / 2, t.rows);
+        return true;
+    }
+    __device__ const uint8_t *x_scales(int K, int k0) const { return a.xs + (int64_t)t.m0 * (K / 32) + k0 / 32; }
+    __device__ void issue(int kt, uint32_t stage) {
+        sl.issue(kt, stage - (uint32_t)((kt % C::NSTAGE) * S8::BYTES));   // chunk first: see ScaleLoader
+        xl.issue(kt * C::BK, stage);
+        wl.issue(kt * C::BK, stage + C::X_BYTES);
+    }
+    __device__ int wrow(int wn, int fn) const { return wn * C::WN + fn * 32; }
+};
+
+struct FfnGateUp8 : Ffn8Base {
+    __device__ bool setup(const Args &args, int b) {
+        int k0;
+        const int H = args.H;
+        if (!begin(args, b, H, k0)) return false;
+        const int i0 = t.nt * (C::BN / 2), nw = min(C::BN / 2, a.I - i0);
+        const int64_t wo = (int64_t)i0 * H + k0, so = (int64_t)i0 * (H / 32) + k0 / 32;
+        wl.init_split_rows(as_pairs(a.w0 + wo), as_pairs(a.w1 + wo), H / 2, nw);
+        sl.init(x_scales(H, k0), t.rows, H / 32, a.w0s + so, nw, H / 32, a.w1s + so);
+        return true;
+    }
+    // gate rows of the W tile pair with the up rows BN/2 further inside one wave
+    __device__ int wrow(int wn, int fn) const {
+        return fn < C::FN / 2 ? wn * (C::WN / 2) + fn * 32 : C::BN / 2 + wn * (C::WN / 2) + (fn - C::FN / 2) * 32;
+    }
+    __device__ void epilogue(f32x16_t (&acc)[C::FM][C::FN], int wm, int wn) {
+        constexpr size_t END = S8::LDS_BYTES;
+        const int I = a.I, ib0 = t.nt * (C::BN / 2) + wn * (C::WN / 2);
+        const bool live = ib0 < I;   // I % 128 == 0: the wave's i are all valid or all past I
+        if (a.splits > 1) {
+            store_partials<C>(acc, a.part + ((int64_t)t.s * a.T + t.m0) * 2 * I, 2 * I, t.rows, wm, live, [&](int fn) {
+                return fn < C::FN / 2 ? ib0 + fn * 32 : I + ib0 + (fn - C::FN / 2) * 32;
+            });
+            return;
+        }
+        if (!live) return;
+        if (a.h) {
+            const uint32_t h_row = 4u * (uint32_t)I;
+            const uint32_t h_col =
+                2u * (uint32_t)(ib0 + (FragStage<C, END>::pass_col(epi_lane()) >= C::WN / 2 ? I - C::WN / 2 : 0));
+            staged_rows<C, END>([&](int fm, int fn, int g4, int j) { return acc[fm][fn][g4 * 4 + j]; },
+                                rows_rsrc(a.h + (int64_t)t.m0 * 2 * I, (uint32_t)t.rows * h_row),
+                                [&](int fm, int r) -> uint32_t {
+                                    return (uint32_t)(wm * C::WM + fm * 32 + r) * h_row + h_col;
+                                });
+        }
+        const int lane = epi_lane();
+#pragma unroll
+        for (int fm = 0; fm < C::FM; ++fm) {
+            const int m = wm * C::WM + fm * 32 + (lane & 31);
+            const bool ok = m < t.rows;   // same for lanes l and l ^ 32
+            uint8_t *el = a.q + (int64_t)(t.m0 + m) * I, *sc = a.qs + (int64_t)(t.m0 + m) * (I / 32);
+#pragma unroll
+            for (int fn = 0; fn < C::FN / 2; ++fn) {
+                const int ib = ib0 + fn * 32;   // one 32-block of i
+                Block16 av;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float hg = acc[fm][fn][e], hu = acc[fm][fn + C::FN / 2][e];
+                    av.v[e] = hg * sigmoidf_(hg) * hu;
+                }
+                const Enc16 q8 = quantize_block16(av);
+                if (ok) {
+#pragma unroll
+                    for (int g4 = 0; g4 < 4; ++g4)
+                        *reinterpret_cast<uint32_t *>(el + ib + g4 * 8 + (lane >> 5) * 4) = q8.enc[g4];
+                    if (lane < 32) sc[ib / 32] = (uint8_t)q8.scale;
+                }
+            }
+        }
+    }
+};
+
+struct FfnDown8 : Ffn8Base {
+    __device__ bool setup(const Args &args, int b) {
+        int k0;
+        const int I = args.I;
+        if (!begin(args, b, I, k0)) return false;
+        const int n0 = t.nt * C::BN, nw = min(C::BN, a.H - n0);
+        wl.init(as_pairs(a.w0 + (int64_t)n0 * I + k0), I / 2, nw);
+        sl.init(x_scales(I, k0), t.rows, I / 32, a.w0s + (int64_t)n0 * (I / 32) + k0 / 32, nw, I / 32);
+        return true;
+    }
+    __device__ void epilogue(f32x16_t (&acc)[C::FM][C::FN], int wm, int wn) {
+        dense_epilogue<C, S8::LDS_BYTES>(acc, t, a.T, a.H, a.splits, wm, wn, a.addend, a.out, a.part);
+    }
+};
+
+struct FfnDA8 : Ffn8Base {
+    __device__ bool setup(const Args &args, int b) {
+        int k0;
+        const int H = args.H;
+        if (!begin(args, b, H, k0)) return false;
+        const int i0 = t.nt * C::BN, nw = min(C::BN, a.I - i0);
+        wl.init(as_pairs(a.w0 + (int64_t)i0 * H + k0), H / 2, nw);
+        sl.init(x_scales(H, k0), t.rows, H / 32, a.w0s + (int64_t)i0 * (H / 32) + k0 / 32, nw, H / 32);
+        return true;
+    }
+    __device__ void epilogue(f32x16_t (&acc)[C::FM][C::FN], int wm, int wn) {
+        const int lane = threadIdx.x & 63;
+        const int I = a.I, ib0 = t.nt * C::BN + wn * C::WN;
+        const bool live = ib0 < I;   // I % 128 == 0: a wave's 64 columns are all valid or none
+        if (a.splits > 1) {
+            store_partials<C>(acc, a.part + ((int64_t)t.s * a.T + t.m0) * I, I, t.rows, wm, live,
+                              [&](int fn) { return ib0 + fn * 32; });
+            return;
+        }
+        if (!live) return;
+#pragma unroll
+        for (int fm = 0; fm < C::FM; ++fm) {
+            const int m = wm * C::WM + fm * 32 + (lane & 31);
+            const bool ok = m < t.rows;
+            const int64_t r = t.m0 + (ok ? m : 0);
+            HBatch<C> h;
+            h.load(a.h_in + r * 2 * I, I, ib0, lane);
+            uint16_t *dhrow = a.dh + r * 2 * I, *arow = a.a + r * I;
+            uint8_t *qrow = a.q + r * 2 * I, *srow = a.qs + r * (2 * I / 32);
+#pragma unroll
+            for (int fn = 0; fn < C::FN; ++fn) {
+                const int ib = ib0 + fn * 32;   // one 32-block of i
+                Block16 dg, du;
+#pragma unroll
+                for (int g4 = 0; g4 < 4; ++g4) {
+                    const int i = ib + g4 * 8 + (lane >> 5) * 4, e = g4 * 4;
+                    float av[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const GluGrad g = glu_backward(acc[fm][fn][e + j], bf16_at(h.g[fn][g4], j), bf16_at(h.u[fn][g4], j));
+                        av[j] = g.a;
+                        dg.v[e + j] = g.dg;
+                        du.v[e + j] = g.du;
+                    }
+                    if (ok) {
+                        store4_bf16(arow + i, av[0], av[1], av[2], av[3]);
+                        store4_bf16(dhrow + i, dg.v[e], dg.v[e + 1], dg.v[e + 2], dg.v[e + 3]);
+                        store4_bf16(dhrow + I + i, du.v[e], du.v[e + 1], du.v[e + 2], du.v[e + 3]);
+                    }
+                }
+                const Enc16 qg = quantize_block16(dg), qu = quantize_block16(du);
+                if (ok) {
+#pragma unroll
+                    for (int g4 = 0; g4 < 4; ++g4) {
+                        const int i = ib + g4 * 8 + (lane >> 5) * 4;
+                        *reinterpret_cast<uint32_t *>(qrow + i) = qg.enc[g4];
+                        *reinterpret_cast<uint32_t *>(qrow + I + i) = qu.enc[g4];
+                    }
+                    if (lane < 32) {
+                        srow[ib / 32] = (uint8_t)qg.scale;
+                        srow[(I + ib) / 32] = (uint8_t)qu.scale;
+                    }
+                }
+            }
+        }
+    }
+};
+
+struct FfnDX8 : Ffn8Base {
+    __device__ bool setup(const Args &args, int b) {
+        int k0;
+        const int I = args.I;
+        if (!begin(args, b, 2 * I, k0)) return false;
+        const int n0 = t.nt * C::BN, nw = min(C::BN, a.H - n0);
+        const int64_t wo = (int64_t)n0 * I, so = (int64_t)n0 * (I / 32);
+        const uint8_t *xs = x_scales(2 * I, k0);
+        if (k0 < I) {   // the run starts among the gate columns and may go on into the up columns
+            wl.init(as_pairs(a.w0 + wo + k0), I / 2, nw, as_pairs(a.w1 + wo), (I - k0) / 2);
+            sl.init(xs, t.rows, 2 * I / 32, a.w0s + so + k0 / 32, nw, I / 32, nullptr, a.w1s + so, I - k0);
+        } else {
+            wl.init(as_pairs(a.w1 + wo + (k0 - I)), I / 2, nw);
+            sl.init(xs, t.rows, 2 * I / 32, a.w1s + so + (k0 - I) / 32, nw, I / 32);
+        }
+        return true;
+    }
+    __device__ void epilogue(f32x16_t (&acc)[C::FM][C::FN], int wm, int wn) {
+        dense_epilogue<C, S8::LDS_BYTES>(acc, t, a.T, a.H, a.splits, wm, wn, a.addend, a.out, a.part);
+    }
+};
+
+// dy along H: a thread takes 8 values, 4 neighbouring lanes one 32-block.
+__global__ __launch_bounds__(256) void ffn_quantize_rows(const uint16_t *__restrict__ src, int64_t n8,
+                                                         uint8_t *__restrict__ el, uint8_t *__restrict__ sc) {
+    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (c >= n8) return;   // whole groups of 4 lanes: rows are multiples of 128 values
+    const uint4 x = reinterpret_cast<const uint4 *>(src)[c];
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t amax = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) amax = max(amax, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+    amax = max(amax, (uint32_t)__shfl_xor((int)amax, 1));
+    amax = max(amax, (uint32_t)__shfl_xor((int)amax, 2));
+    const uint32_t sb = mx_scale_byte_bf16(amax);
+    const int e = (int)sb - 127;
+    reinterpret_cast<uint2 *>(el)[c] = make_uint2(e4m3x4_bf16(w[0], w[1], e), e4m3x4_bf16(w[2], w[3], e));
+    if ((c & 3) == 0) sc[c >> 2] = (uint8_t)sb;
+}
+
+template <class P>
+__global__ __launch_bounds__(CfgA::NT, 2) void ffn_gemm8(Ffn8Args args) {
+    extern __shared__ __attribute__((aligned(1024))) char lds_raw[];
+    P p;
+    if (!p.setup(args, (int)blockIdx.x)) return;
+    gemm8_tile(p, (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds_raw);
+}
+
+// dW_gate | dW_up and dW_down (BF16 tiles), then dx (block-scaled tiles), in one launch.
+template <class PW>
+__global__ __launch_bounds__(CfgA::NT, 2) void ffn_grads8(FfnWgradArgs gu, FfnWgradArgs wd, Ffn8Args ax, int g0, int g1) {
+    extern __shared__ __attribute__((aligned(1024))) char lds_raw[];
+    const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds_raw;
+    int b = (int)blockIdx.x;
+    if (b < g0 + g1) {
+        PW p;
+        if (!p.setup(b < g0 ? gu : wd, b < g0 ? b : b - g0)) return;
+        gemm_tile(p, lds);
+    } else {
+        FfnDX8 p;
+        if (!p.setup(ax, b - g0 - g1)) return;
+        gemm8_tile(p, lds);
+    }
+}
+
+template <class P>
+hipError_t product8(const char *name, const FfnSplit &s, Ffn8Args a, int n_tiles, hipStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    const hipError_t e = allow_lds(ffn_gemm8<P>, S8::LDS_BYTES, done);
+    if (e != hipSuccess) return e;
+    a.n_tiles = n_tiles;
+    a.splits = s.splits;
+    a.len = s.len;
+    KernelTimer tm(name, st);
+    ffn_gemm8<P><<<ffn_grid(a.T, s.bm, n_tiles, s.splits), CfgA::NT, S8::LDS_BYTES, st>>>(a);
+    return hipGetLastError();
+}
+
+template <class CW>
+hipError_t launch_grads8(const FfnWgradArgs &gu, const FfnWgradArgs &wd, const Ffn8Args &ax, hipStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    auto *k = ffn_grads8<FfnWgrad<CW>>;
+    constexpr size_t lds = S8::LDS_BYTES > CW::LDS_BYTES ? S8::LDS_BYTES : CW::LDS_BYTES;
+    const hipError_t e = allow_lds(k, lds, done);
+    if (e != hipSuccess) return e;
+    const unsigned g0 = wgrad_grid(gu.M, gu.N, CW::BM), g1 = wgrad_grid(wd.M, wd.N, CW::BM);
+    const unsigned gx = ffn_grid(ax.T, CfgA::BM, ax.n_tiles, ax.splits);
+    KernelTimer tm("ffn_grads_mx", st);
+    k<<<g0 + g1 + gx, CfgA::NT, lds, st>>>(gu, wd, ax, (int)g0, (int)g1);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t ffn_mx_forward(const FfnPlan &p, char *ws, const uint8_t *x_elems, const uint8_t *x_scales,
+                          const mok_weights &w, const uint16_t *addend, uint16_t *out, uint16_t *h, hipStream_t st) {
+    Ffn8Args a{};
+    a.T = (int)p.T;
+    a.H = p.H;
+    a.I = p.I;
+    a.x = x_elems;
+    a.xs = x_scales;
+    a.w0 = w.gate_elems;
+    a.w0s = w.gate_scales;
+    a.w1 = w.up_elems;
+    a.w1s = w.up_scales;
+    a.h = h;
+    a.q = reinterpret_cast<uint8_t *>(ws + p.a_q);
+    a.qs = reinterpret_cast<uint8_t *>(ws + p.a_qs);
+    a.part = reinterpret_cast<float *>(ws + p.part);
+    hipError_t e = product8<FfnGateUp8>("ffn_gate_up_mx", p.gate_up, a, (int)ceil_div(p.I, kTileN / 2), st);
+    if (e != hipSuccess) return e;
+    if (p.gate_up.splits > 1) {
+        KernelTimer tm("ffn_join_act", st);
+        ffn_join_act<true><<<join_grid(p.T, p.I), 256, 0, st>>>(a.part, p.gate_up.splits, a.T, a.I, h, nullptr, a.q, a.qs);
+    }
+    a.x = a.q;
+    a.xs = a.qs;
+    a.w0 = w.down_elems;
+    a.w0s = w.down_scales;
+    a.addend = addend;
+    a.out = out;
+    e = product8<FfnDown8>("ffn_down_mx", p.down, a, (int)ceil_div(p.H, kTileN), st);
+    if (e == hipSuccess && p.down.splits > 1) {
+        KernelTimer tm("ffn_join_out", st);
+        ffn_join_out<<<join_grid(p.T, p.H), 256, 0, st>>>(a.part, p.down.splits, a.T, a.H, addend, out);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+hipError_t ffn_mx_backward(const FfnPlan &p, char *ws, const uint16_t *x, const mok_weights &w, const uint16_t *h,
+                           const uint16_t *dy, const uint16_t *addend, uint16_t *dx, uint16_t *dw_gate, uint16_t *dw_up,
+                           uint16_t *dw_down, hipStream_t st) {
+    Ffn8Args a{};
+    a.T = (int)p.T;
+    a.H = p.H;
+    a.I = p.I;
+    a.a = reinterpret_cast<uint16_t *>(ws + p.a);
+    a.dh = reinterpret_cast<uint16_t *>(ws + p.dh);
+    a.q = reinterpret_cast<uint8_t *>(ws + p.dh_q);
+    a.qs = reinterpret_cast<uint8_t *>(ws + p.dh_qs);
+    a.part = reinterpret_cast<float *>(ws + p.part);
+    hipError_t e = hipSuccess;
+    if (p.T > 0) {
+        uint8_t *dyq = reinterpret_cast<uint8_t *>(ws + p.dy_q), *dyqs = reinterpret_cast<uint8_t *>(ws + p.dy_qs);
+        {
+            const int64_t n8 = p.T * (int64_t)p.H / 8;
+            KernelTimer tm("ffn_quantize_rows", st);
+            ffn_quantize_rows<<<(unsigned)ceil_div(n8, 256), 256, 0, st>>>(dy, n8, dyq, dyqs);
+        }
+        a.x = dyq;
+        a.xs = dyqs;
+        a.w0 = w.down_elems;
+        a.w0s = w.down_scales;
+        a.h_in = h;
+        e = product8<FfnDA8>("ffn_da_mx", p.da, a, (int)ceil_div(p.I, kTileN), st);
+        if (e != hipSuccess) return e;
+        if (p.da.splits > 1) {
+            KernelTimer tm("ffn_join_da", st);
+            ffn_join_da<true><<<join_grid(p.T, p.I), 256, 0, st>>>(a.part, p.da.splits, a.T, a.I, h, a.dh, a.a, a.q, a.qs);
+        }
+    }
+    a.x = a.q;
+    a.xs = a.qs;
+    a.w0 = w.gate_elems;
+    a.w0s = w.gate_scales;
+    a.w1 = w.up_elems;
+    a.w1s = w.up_scales;
+    a.addend = addend;
+    a.out = dx;
+    a.n_tiles = (int)ceil_div(p.H, kTileN);
+    a.splits = p.dx.splits;
+    a.len = p.dx.len;
+    const FfnWgradArgs gu{a.T, p.H, 2 * p.I, p.I, p.I, x, a.dh, dw_gate, dw_up};
+    const FfnWgradArgs wd{a.T, p.I, p.H, p.H, p.H, a.a, dy, dw_down, nullptr};
+    e = p.wgrad_bm == CfgS::BM ? launch_grads8<CfgS>(gu, wd, a, st) : launch_grads8<CfgA>(gu, wd, a, st);
+    if (e == hipSuccess && p.T > 0 && p.dx.splits > 1) {
+        KernelTimer tm("ffn_join_out", st);
+        ffn_join_out<<<join_grid(p.T, p.H), 256, 0, st>>>(a.part, p.dx.splits, a.T, a.H, addend, dx);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+}  // namespace mok

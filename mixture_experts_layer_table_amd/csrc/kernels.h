@@ -35,4 +35,54 @@ mok_status launch_route(const float *logits, int64_t T, int E, int k, int32_t *i
 mok_status launch_route_backward(const int32_t *ids, const float *w, const float *dw, int64_t T, int E, int k,
                                  float *dl, hipStream_t st);
 
+mok_status launch_dropout(const uint16_t *x, const void *residual, int64_t n, float p, const uint64_t *rng,
+                          bool f32_stream, void *out, hipStream_t st);
+
+mok_status launch_dropout_backward(const void *dy, int64_t n, float p, const uint64_t *rng, bool f32_stream,
+                                   uint16_t *dx, hipStream_t st);
+
+constexpr int kNormMaxH = 16384;   // 16 waves x 2 chunks of 8 elements per lane
+
+struct NormCall {
+    int64_t T;
+    int H;
+    float eps, p;
+    bool f32_stream;
+    const uint16_t *x;
+    const void *residual;
+    const uint16_t *weight;
+    const uint64_t *rng;
+    void *sum;
+    uint16_t *y;
+    uint8_t *elems, *scales;
+    float *rstd;
+};
+mok_status launch_add_rmsnorm(const NormCall &c, hipStream_t st);
+
+struct NormBackwardCall {
+    int64_t T;
+    int H;
+    float p;
+    bool f32_stream;
+    const uint16_t *dy;
+    const void *sum, *dsum;
+    const uint16_t *weight;
+    const float *rstd;
+    const uint64_t *rng;
+    void *dres;
+    uint16_t *dx;
+    float *dweight;
+    float *part;   // norm_backward_blocks(T) x H floats
+};
+int norm_backward_blocks(int64_t T);
+mok_status launch_add_rmsnorm_backward(const NormBackwardCall &c, hipStream_t st);
+
+struct FfnPlan;
+mok_status launch_ffn_forward(const FfnPlan &p, void *workspace, const uint16_t *x, const uint8_t *x_elems,
+                              const uint8_t *x_scales, const mok_weights &w, const uint16_t *addend, uint16_t *out,
+                              uint16_t *h, hipStream_t st);
+mok_status launch_ffn_backward(const FfnPlan &p, void *workspace, const uint16_t *x, const mok_weights &w,
+                               const uint16_t *h, const uint16_t *dy, const uint16_t *addend, uint16_t *dx,
+                               uint16_t *dw_gate, uint16_t *dw_up, uint16_t *dw_down, hipStream_t st);
+
 }  // namespace mok

@@ -24,10 +24,12 @@ Modules:
   mxfp8     — O4, the MXFP8 codec and fake-quant
   router    — O5, the router front-end (softmax, top-k, renormalisation) and
               its logit gradient
+  block     — O6, the operators around the routed experts (dropout, residual
+              RMS norm, gated feed-forward block)
 
 Parity status: every function here is pinned by ``tests/test_oracle_*.py``
 against values fixed outside the oracle (closed forms, brute force, finite
 differences, an independent autograd formulation, library casts); none is
 "parity unpinned".
 """
-from . import schedule, layer, mxfp8, router  # noqa: F401
+from . import schedule, layer, mxfp8, router, block  # noqa: F401
