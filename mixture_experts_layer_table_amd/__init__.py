@@ -592,28 +592,51 @@ def route_backward(topk_ids, topk_w, dtopk_w, E: int):
 # ----------------------------------------------------------------------------- around the routed experts
 
 _STREAM_DTYPES = {torch.bfloat16: MOK_STREAM_BF16, torch.float32: MOK_STREAM_F32}
+_BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
 
 
-def _on_device(t):
-    """(current stream of t's device, guard that makes that device current): the
-    kernels go to the device that holds the tensors, whatever device is current."""
-    if t.device.type != "cuda":
-        raise ValueError(f"tensors must be on a GPU, got {t.device}")
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream), torch.cuda.device(t.device)
+# These calls are short: for one decoded token the kernels take 3 to 25 us, so
+# the host's share shows. The checks test the common case inline and leave the
+# error's wording to _require; pointers go to ctypes as plain integers.
+
+def _need(t, name, dtype, shape, device):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.device == device):
+        _require(t, name, dtype, shape, device)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _elsewhere(device) -> bool:
+    """Whether device is not the current one: the kernels go to the device that
+    holds the tensors, whatever device is current."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, got {device}")
+    return torch.cuda.current_device() != device.index
+
+
+# torch.cuda.current_stream() builds a Stream object (1.9 us); the handle alone takes 0.1 us.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _stream_dtype(dtype, name):
-    if dtype not in _STREAM_DTYPES:
+    sd = _STREAM_DTYPES.get(dtype)
+    if sd is None:
         raise ValueError(f"{name}: dtype {dtype}, expected torch.bfloat16 or torch.float32")
-    return _STREAM_DTYPES[dtype]
+    return sd
 
 
-def _check_rng(p, rng, device):
+def _rng_addr(p, rng, device):
     """rng: int64 [2] on the device, {seed, offset} as bit patterns; unused when p == 0."""
     if not 0.0 <= p < 1.0:
         raise ValueError(f"p: {p}, expected a value in [0, 1)")
-    if p > 0.0:
-        _require(rng, "rng", torch.int64, (2,), device)
+    if p == 0.0:
+        return None
+    _need(rng, "rng", torch.int64, (2,), device)
+    return rng.data_ptr()
 
 
 def dropout(x, rng, p: float, residual=None, out=None):
@@ -621,37 +644,41 @@ def dropout(x, rng, p: float, residual=None, out=None):
     fp32 of that shape, or None; rng: int64 [2] on the device, {seed, offset}.
     Returns a tensor of residual's type (bf16 without one); ``out`` may be
     residual. A call draws (x.numel() + 3) // 4 counters from offset on."""
-    shape, dev = tuple(x.shape), x.device
-    _require(x, "x", torch.bfloat16, shape)
-    dtype = torch.bfloat16 if residual is None else residual.dtype
-    sd = _stream_dtype(dtype, "residual")
+    shape, dev = x.shape, x.device
+    like = x if residual is None else residual
+    sd = _stream_dtype(like.dtype, "residual")
+    _need(x, "x", _BF16, shape, dev)
     if residual is not None:
-        _require(residual, "residual", dtype, shape, dev)
-    _check_rng(p, rng, dev)
-    st, guard = _on_device(x)
-    with guard:
-        if out is None:
-            out = torch.empty(shape, dtype=dtype, device=dev)
-        else:
-            _require(out, "out", dtype, shape, dev)
-        _check(mok_dropout(_ptr(x), _ptr(residual), x.numel(), p, _ptr(rng), sd, _ptr(out), st), "mok_dropout")
+        _need(residual, "residual", residual.dtype, shape, dev)
+    state = _rng_addr(p, rng, dev)
+    if out is not None:
+        _need(out, "out", like.dtype, shape, dev)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return dropout(x, rng, p, residual, out)
+    if out is None:
+        out = torch.empty_like(like)
+    _check(_lib.mok_dropout(x.data_ptr(), _addr(residual), x.numel(), p, state, sd, out.data_ptr(), _raw_stream(dev.index)),
+           "mok_dropout")
     return out
 
 
 def dropout_backward(dy, rng, p: float, dx=None):
     """Gradient of dropout() with respect to x, bf16 (mok_dropout_backward); p and
     rng as the forward had them. The residual's gradient is dy itself."""
-    shape, dev = tuple(dy.shape), dy.device
+    shape, dev = dy.shape, dy.device
     sd = _stream_dtype(dy.dtype, "dy")
-    _require(dy, "dy", dy.dtype, shape)
-    _check_rng(p, rng, dev)
-    st, guard = _on_device(dy)
-    with guard:
-        if dx is None:
-            dx = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        else:
-            _require(dx, "dx", torch.bfloat16, shape, dev)
-        _check(mok_dropout_backward(_ptr(dy), dy.numel(), p, _ptr(rng), sd, _ptr(dx), st), "mok_dropout_backward")
+    _need(dy, "dy", dy.dtype, shape, dev)
+    state = _rng_addr(p, rng, dev)
+    if dx is not None:
+        _need(dx, "dx", _BF16, shape, dev)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return dropout_backward(dy, rng, p, dx)
+    if dx is None:
+        dx = torch.empty_like(dy, dtype=_BF16)
+    _check(_lib.mok_dropout_backward(dy.data_ptr(), dy.numel(), p, state, sd, dx.data_ptr(), _raw_stream(dev.index)),
+           "mok_dropout_backward")
     return dx
 
 
@@ -663,36 +690,46 @@ def add_rmsnorm(x, weight, eps: float, residual=None, p: float = 0.0, rng=None, 
     dict: sum [T, H] in the stream's type, rstd fp32 [T], y bf16 [T, H] (if
     ``y``), y_elems uint8 [T, H] and y_scales uint8 [T, H/32] (if ``mxfp8``).
     ``outs``: the same keys, caller-given; sum may be residual."""
-    if x.dim() != 2:
-        raise ValueError(f"x: shape {tuple(x.shape)}, expected [T, H]")
-    T, H = x.shape
-    dev = x.device
-    dtype = stream_dtype or (torch.bfloat16 if residual is None else residual.dtype)
+    shape, dev = x.shape, x.device
+    if len(shape) != 2:
+        raise ValueError(f"x: shape {tuple(shape)}, expected [T, H]")
+    T, H = shape
+    dtype = stream_dtype or (_BF16 if residual is None else residual.dtype)
     sd = _stream_dtype(dtype, "stream_dtype")
-    _require(x, "x", torch.bfloat16, (T, H))
-    _require(weight, "weight", torch.bfloat16, (H,), dev)
+    _need(x, "x", _BF16, shape, dev)
+    _need(weight, "weight", _BF16, (H,), dev)
     if residual is not None:
-        _require(residual, "residual", dtype, (T, H), dev)
-    _check_rng(p, rng, dev)
-    shapes = dict(sum=((T, H), dtype), rstd=((T,), torch.float32))
-    if y:
-        shapes["y"] = ((T, H), torch.bfloat16)
-    if mxfp8:
-        if H % 32:
-            raise ValueError(f"x: H = {H}, MXFP8 rows need a multiple of 32")
-        shapes["y_elems"], shapes["y_scales"] = ((T, H), torch.uint8), ((T, H // 32), torch.uint8)
-    st, guard = _on_device(x)
-    with guard:
-        if outs is None:
-            outs = {n: torch.empty(sh, dtype=dt, device=dev) for n, (sh, dt) in shapes.items()}
-        else:
-            for n, (sh, dt) in shapes.items():
-                _require(outs.get(n), n, dt, sh, dev)
-            outs = {n: outs[n] for n in shapes}
-        _check(mok_add_rmsnorm(mok_norm_shape(T, H, sd, eps, p), _ptr(x), _ptr(residual), _ptr(weight), _ptr(rng),
-                               _ptr(outs["sum"]), _ptr(outs.get("y")), _ptr(outs.get("y_elems")),
-                               _ptr(outs.get("y_scales")), _ptr(outs["rstd"]), st), "mok_add_rmsnorm")
-    return outs
+        _need(residual, "residual", dtype, shape, dev)
+    state = _rng_addr(p, rng, dev)
+    if not y and not mxfp8:
+        raise ValueError("y and mxfp8 are both off: nothing to write")
+    if mxfp8 and H % 32:
+        raise ValueError(f"x: H = {H}, MXFP8 rows need a multiple of 32")
+    if outs is not None:
+        _need(outs.get("sum"), "sum", dtype, shape, dev)
+        _need(outs.get("rstd"), "rstd", _F32, (T,), dev)
+        if y:
+            _need(outs.get("y"), "y", _BF16, shape, dev)
+        if mxfp8:
+            _need(outs.get("y_elems"), "y_elems", _U8, shape, dev)
+            _need(outs.get("y_scales"), "y_scales", _U8, (T, H // 32), dev)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return add_rmsnorm(x, weight, eps, residual, p, rng, stream_dtype, y, mxfp8, outs)
+    if outs is None:
+        r = dict(sum=torch.empty_like(x, dtype=dtype), rstd=x.new_empty((T,), dtype=_F32))
+        if y:
+            r["y"] = torch.empty_like(x)
+        if mxfp8:
+            r["y_elems"], r["y_scales"] = torch.empty_like(x, dtype=_U8), x.new_empty((T, H // 32), dtype=_U8)
+    else:
+        r = {n: outs[n] for n in ("sum", "rstd") + (("y",) if y else ()) + (("y_elems", "y_scales") if mxfp8 else ())}
+    _check(_lib.mok_add_rmsnorm(ctypes.byref(mok_norm_shape(T, H, sd, eps, p)), x.data_ptr(), _addr(residual),
+                                weight.data_ptr(), state, r["sum"].data_ptr(), r["y"].data_ptr() if y else None,
+                                r["y_elems"].data_ptr() if mxfp8 else None,
+                                r["y_scales"].data_ptr() if mxfp8 else None, r["rstd"].data_ptr(), _raw_stream(dev.index)),
+           "mok_add_rmsnorm")
+    return r
 
 
 def add_rmsnorm_backward(dy, sum, weight, rstd, dsum=None, p: float = 0.0, rng=None, grads=None, workspace=None):
@@ -701,43 +738,47 @@ def add_rmsnorm_backward(dy, sum, weight, rstd, dsum=None, p: float = 0.0, rng=N
     stream, or None. Returns a dict: dresidual [T, H] in sum's type, dx bf16
     [T, H] (the same tensor as dresidual where both are bf16 and p == 0),
     dweight fp32 [H]. ``workspace``: uint8, made here if None."""
-    if sum.dim() != 2:
-        raise ValueError(f"sum: shape {tuple(sum.shape)}, expected [T, H]")
-    T, H = sum.shape
-    dev, dtype = sum.device, sum.dtype
+    shape, dev, dtype = sum.shape, sum.device, sum.dtype
+    if len(shape) != 2:
+        raise ValueError(f"sum: shape {tuple(shape)}, expected [T, H]")
+    T, H = shape
     sd = _stream_dtype(dtype, "sum")
-    _require(sum, "sum", dtype, (T, H))
-    _require(dy, "dy", torch.bfloat16, (T, H), dev)
-    _require(weight, "weight", torch.bfloat16, (H,), dev)
-    _require(rstd, "rstd", torch.float32, (T,), dev)
+    _need(sum, "sum", dtype, shape, dev)
+    _need(dy, "dy", _BF16, shape, dev)
+    _need(weight, "weight", _BF16, (H,), dev)
+    _need(rstd, "rstd", _F32, (T,), dev)
     if dsum is not None:
-        _require(dsum, "dsum", dtype, (T, H), dev)
-    _check_rng(p, rng, dev)
-    shape = mok_norm_shape(T, H, sd, 0.0, p)
+        _need(dsum, "dsum", dtype, shape, dev)
+    state = _rng_addr(p, rng, dev)
+    separate = p > 0.0 or dtype is not _BF16
+    if grads is not None:
+        _need(grads.get("dresidual"), "dresidual", dtype, shape, dev)
+        _need(grads.get("dweight"), "dweight", _F32, (H,), dev)
+        if separate:
+            _need(grads.get("dx"), "dx", _BF16, shape, dev)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return add_rmsnorm_backward(dy, sum, weight, rstd, dsum, p, rng, grads, workspace)
+    s = mok_norm_shape(T, H, sd, 0.0, p)
     need = ctypes.c_size_t()
-    _check(mok_add_rmsnorm_backward_size(shape, ctypes.byref(need)), "mok_add_rmsnorm_backward_size")
-    separate = p > 0.0 or dtype != torch.bfloat16
-    shapes = dict(dresidual=((T, H), dtype), dweight=((H,), torch.float32))
-    if separate:
-        shapes["dx"] = ((T, H), torch.bfloat16)
-    st, guard = _on_device(sum)
-    with guard:
-        if workspace is None:
-            workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
+    _check(_lib.mok_add_rmsnorm_backward_size(ctypes.byref(s), ctypes.byref(need)), "mok_add_rmsnorm_backward_size")
+    if workspace is None:
+        workspace = sum.new_empty((need.value,), dtype=_U8)
+    else:
         _require_bytes(workspace, "workspace", need.value, dev)
-        if grads is None:
-            grads = {n: torch.empty(sh, dtype=dt, device=dev) for n, (sh, dt) in shapes.items()}
-        else:
-            for n, (sh, dt) in shapes.items():
-                _require(grads.get(n), n, dt, sh, dev)
-            grads = {n: grads[n] for n in shapes}
-        _check(mok_add_rmsnorm_backward(shape, _ptr(workspace), workspace.numel(), _ptr(dy), _ptr(sum), _ptr(weight),
-                                        _ptr(rstd), _ptr(dsum), _ptr(rng), _ptr(grads["dresidual"]),
-                                        _ptr(grads.get("dx")), _ptr(grads["dweight"]), st),
-               "mok_add_rmsnorm_backward")
+    if grads is None:
+        g = dict(dresidual=torch.empty_like(sum), dweight=sum.new_empty((H,), dtype=_F32))
+        if separate:
+            g["dx"] = torch.empty_like(dy)
+    else:
+        g = {n: grads[n] for n in ("dresidual", "dweight") + (("dx",) if separate else ())}
+    _check(_lib.mok_add_rmsnorm_backward(ctypes.byref(s), workspace.data_ptr(), workspace.numel(), dy.data_ptr(),
+                                         sum.data_ptr(), weight.data_ptr(), rstd.data_ptr(), _addr(dsum), state,
+                                         g["dresidual"].data_ptr(), g["dx"].data_ptr() if separate else None,
+                                         g["dweight"].data_ptr(), _raw_stream(dev.index)), "mok_add_rmsnorm_backward")
     if not separate:
-        grads["dx"] = grads["dresidual"]
-    return grads
+        g["dx"] = g["dresidual"]
+    return g
 
 
 @dataclasses.dataclass
@@ -769,13 +810,15 @@ def _check_ffn_weights(ws: FfnWorkspace, weights: mok_weights, orientation: str)
     kind = getattr(weights, "_kind", "")
 
     def one(t, name, dtype, shape):
-        _require(t, name, dtype, (1,) + shape if isinstance(t, torch.Tensor) and t.dim() == 3 else shape, dev)
+        _need(t, name, dtype, (1,) + shape if t.dim() == 3 else shape, dev)
 
     if ws.precision == MOK_BF16:
         if not kind.startswith("bf16"):
             raise ValueError("BF16 mode needs bf16 weights (weights_bf16)")
-        for t, n, sh in zip(tensors, ("w_gate", "w_up", "w_down"), ((H, I), (H, I), (I, H))):
-            one(t, n, torch.bfloat16, sh)
+        g, u, d = tensors
+        one(g, "w_gate", _BF16, (H, I))
+        one(u, "w_up", _BF16, (H, I))
+        one(d, "w_down", _BF16, (I, H))
         return
     if not kind.startswith("mxfp8"):
         raise ValueError("MXFP8 mode needs quantized weights (MXFP8Weights)")
@@ -783,8 +826,8 @@ def _check_ffn_weights(ws: FfnWorkspace, weights: mok_weights, orientation: str)
         raise ValueError(f"MXFP8 weights quantized for {kind.split(':')[1]}, used in {orientation}")
     shapes = ((I, H), (I, H), (H, I)) if orientation == "fwd" else ((H, I), (H, I), (I, H))
     for (el, sc), n, sh in zip(tensors, ("gate", "up", "down"), shapes):
-        one(el, n + " elements", torch.uint8, sh)
-        one(sc, n + " scales", torch.uint8, (sh[0], sh[1] // 32))
+        one(el, n + " elements", _U8, sh)
+        one(sc, n + " scales", _U8, (sh[0], sh[1] // 32))
 
 
 def _ffn_rows(ws: FfnWorkspace, t, name):
@@ -799,36 +842,38 @@ def ffn_forward(ws: FfnWorkspace, x, weights: mok_weights, addend=None, out=None
     MXFP8 the pair (elems uint8 [T, H], scales uint8 [T, H/32]) that
     add_rmsnorm(mxfp8=True) or mxfp8_quantize gives. addend: bf16 [T, H] or None;
     ``out`` may be addend. Returns (out bf16 [T, H], h bf16 [T, 2I] for the
-    backward, or None with save_h=False)."""
-    dev, H, I = ws.buffer.device, ws.H, ws.I
-    elems = scales = rows = None
+    backward, or None with save_h=False and no ``h``)."""
+    buf, H, I = ws.buffer, ws.H, ws.I
+    dev = buf.device
     if ws.precision == MOK_BF16:
         T = _ffn_rows(ws, x, "x")
-        _require(x, "x", torch.bfloat16, (T, H), dev)
-        rows = x
+        _need(x, "x", _BF16, (T, H), dev)
+        rows, elems, scales = x.data_ptr(), None, None
     else:
         if not isinstance(x, (tuple, list)) or len(x) != 2:
             raise ValueError("x: MXFP8 mode takes (elems, scales)")
-        elems, scales = x
-        T = _ffn_rows(ws, elems, "x elements")
-        _require(elems, "x elements", torch.uint8, (T, H), dev)
-        _require(scales, "x scales", torch.uint8, (T, H // 32), dev)
+        el, sc = x
+        T = _ffn_rows(ws, el, "x elements")
+        _need(el, "x elements", _U8, (T, H), dev)
+        _need(sc, "x scales", _U8, (T, H // 32), dev)
+        rows, elems, scales = None, el.data_ptr(), sc.data_ptr()
     _check_ffn_weights(ws, weights, "fwd")
     if addend is not None:
-        _require(addend, "addend", torch.bfloat16, (T, H), dev)
-    st, guard = _on_device(ws.buffer)
-    with guard:
-        if out is None:
-            out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-        else:
-            _require(out, "out", torch.bfloat16, (T, H), dev)
-        if h is not None:
-            _require(h, "h", torch.bfloat16, (T, 2 * I), dev)
-        elif save_h:
-            h = torch.empty((T, 2 * I), dtype=torch.bfloat16, device=dev)
-        _check(mok_ffn_forward(mok_ffn_shape(T, H, I, ws.precision), _ptr(ws.buffer), ws.buffer.numel(), _ptr(rows),
-                               _ptr(elems), _ptr(scales), weights, _ptr(addend), _ptr(out), _ptr(h), st),
-               "mok_ffn_forward")
+        _need(addend, "addend", _BF16, (T, H), dev)
+    if out is not None:
+        _need(out, "out", _BF16, (T, H), dev)
+    if h is not None:
+        _need(h, "h", _BF16, (T, 2 * I), dev)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return ffn_forward(ws, x, weights, addend, out, h, save_h)
+    if out is None:
+        out = buf.new_empty((T, H), dtype=_BF16)
+    if h is None and save_h:
+        h = buf.new_empty((T, 2 * I), dtype=_BF16)
+    _check(_lib.mok_ffn_forward(ctypes.byref(mok_ffn_shape(T, H, I, ws.precision)), buf.data_ptr(), buf.numel(), rows,
+                                elems, scales, ctypes.byref(weights), _addr(addend), out.data_ptr(), _addr(h),
+                                _raw_stream(dev.index)), "mok_ffn_forward")
     return out, h
 
 
@@ -837,26 +882,28 @@ def ffn_backward(ws: FfnWorkspace, x, weights: mok_weights, h, dy, addend=None, 
     precision; weights: in MXFP8 the backward's orientation; addend: bf16 [T, H]
     added to dx, or None. Returns dict(dx, dw_gate, dw_up, dw_down), bf16;
     ``grads``: the same keys, caller-given (dx may be addend)."""
-    dev, H, I = ws.buffer.device, ws.H, ws.I
+    buf, H, I = ws.buffer, ws.H, ws.I
+    dev = buf.device
     T = _ffn_rows(ws, x, "x")
-    _require(x, "x", torch.bfloat16, (T, H), dev)
-    _require(h, "h", torch.bfloat16, (T, 2 * I), dev)
-    _require(dy, "dy", torch.bfloat16, (T, H), dev)
+    _need(x, "x", _BF16, (T, H), dev)
+    _need(h, "h", _BF16, (T, 2 * I), dev)
+    _need(dy, "dy", _BF16, (T, H), dev)
     if addend is not None:
-        _require(addend, "addend", torch.bfloat16, (T, H), dev)
+        _need(addend, "addend", _BF16, (T, H), dev)
     _check_ffn_weights(ws, weights, "bwd")
     shapes = dict(dx=(T, H), dw_gate=(H, I), dw_up=(H, I), dw_down=(I, H))
-    st, guard = _on_device(ws.buffer)
-    with guard:
-        if grads is None:
-            grads = {n: torch.empty(sh, dtype=torch.bfloat16, device=dev) for n, sh in shapes.items()}
-        else:
-            for n, sh in shapes.items():
-                _require(grads.get(n), n, torch.bfloat16, sh, dev)
-        _check(mok_ffn_backward(mok_ffn_shape(T, H, I, ws.precision), _ptr(ws.buffer), ws.buffer.numel(), _ptr(x),
-                                weights, _ptr(h), _ptr(dy), _ptr(addend), _ptr(grads["dx"]), _ptr(grads["dw_gate"]),
-                                _ptr(grads["dw_up"]), _ptr(grads["dw_down"]), st), "mok_ffn_backward")
-    return grads
+    if grads is not None:
+        for n, sh in shapes.items():
+            _need(grads.get(n), n, _BF16, sh, dev)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return ffn_backward(ws, x, weights, h, dy, addend, grads)
+    g = {n: buf.new_empty(sh, dtype=_BF16) if grads is None else grads[n] for n, sh in shapes.items()}
+    _check(_lib.mok_ffn_backward(ctypes.byref(mok_ffn_shape(T, H, I, ws.precision)), buf.data_ptr(), buf.numel(),
+                                 x.data_ptr(), ctypes.byref(weights), h.data_ptr(), dy.data_ptr(), _addr(addend),
+                                 g["dx"].data_ptr(), g["dw_gate"].data_ptr(), g["dw_up"].data_ptr(),
+                                 g["dw_down"].data_ptr(), _raw_stream(dev.index)), "mok_ffn_backward")
+    return g
 
 
 def read_schedule(schedule, layout: mok_schedule_layout, E: int):

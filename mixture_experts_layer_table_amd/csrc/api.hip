@@ -290,7 +290,7 @@ mok_status mok_add_rmsnorm(const mok_norm_shape *shape, const void *x, const voi
 
 mok_status mok_add_rmsnorm_backward_size(const mok_norm_shape *shape, size_t *workspace_bytes) {
     if (!norm_shape_ok(shape) || !workspace_bytes) return MOK_ERROR_INVALID_VALUE;
-    *workspace_bytes = std::max<size_t>(256, (size_t)norm_backward_blocks(shape->T) * shape->H * 4);
+    *workspace_bytes = std::max<size_t>(256, (size_t)norm_backward_shares(shape->T, shape->H) * shape->H * 4);
     return MOK_OK;
 }
 

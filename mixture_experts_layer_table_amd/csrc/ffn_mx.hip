@@ -21,6 +21,22 @@ using S8 = Fp8Stage<CfgA>;
 
 __device__ __forceinline__ const uint16_t *as_pairs(const uint8_t *p) { return reinterpret_cast<const uint16_t *>(p); }
 
+// MXFP8 codes staged in a FragStage array: 8-byte unit u of row r holds 8
+// consecutive columns, 4 from lane half 0 and 4 from lane half 1.
+template <class FS>
+__device__ __forceinline__ uint32_t code_off(int r, int u, int lane) {
+    return FS::at(r, u) + (uint32_t)((lane >> 5) * 4);
+}
+__device__ __forceinline__ void put4(uint32_t a, uint32_t v) {
+    *reinterpret_cast<__attribute__((address_space(3))) uint32_t *>((uintptr_t)a) = v;
+}
+__device__ __forceinline__ void bstore1(brsrc_t r, uint32_t voff, uint32_t v) {
+    __builtin_amdgcn_raw_buffer_store_b8((uint8_t)v, r, (int)voff, 0, 0);
+}
+__device__ __forceinline__ void bstore2(brsrc_t r, uint32_t voff, uint32_t v) {
+    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)v, r, (int)voff, 0, 0);
+}
+
 struct Ffn8Args {
     int T, H, I, n_tiles, splits, len;
     const uint8_t *x, *xs;                // the product's row operand and its scales
@@ -97,29 +113,33 @@ struct FfnGateUp8 : Ffn8Base {
                                     return (uint32_t)(wm * C::WM + fm * 32 + r) * h_row + h_col;
                                 });
         }
+        // a: codes of one 32-block of i per row, staged as rows of 32 bytes
+        using FS = FragStage<C, END>;
+        static_assert(C::FN == 2, "one gate and one up block of 32 columns per wave");
         const int lane = epi_lane();
+        const uint32_t area = FS::area(wave_id(), 1);
+        const brsrc_t qres = rows_rsrc(a.q + (int64_t)t.m0 * I, (uint32_t)t.rows * (uint32_t)I);
+        const brsrc_t sres = rows_rsrc(a.qs + (int64_t)t.m0 * (I / 32), (uint32_t)t.rows * (uint32_t)(I / 32));
 #pragma unroll
         for (int fm = 0; fm < C::FM; ++fm) {
-            const int m = wm * C::WM + fm * 32 + (lane & 31);
-            const bool ok = m < t.rows;   // same for lanes l and l ^ 32
-            uint8_t *el = a.q + (int64_t)(t.m0 + m) * I, *sc = a.qs + (int64_t)(t.m0 + m) * (I / 32);
+            const uint32_t m0 = (uint32_t)(wm * C::WM + fm * 32);
+            Block16 av;
 #pragma unroll
-            for (int fn = 0; fn < C::FN / 2; ++fn) {
-                const int ib = ib0 + fn * 32;   // one 32-block of i
-                Block16 av;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float hg = acc[fm][fn][e], hu = acc[fm][fn + C::FN / 2][e];
-                    av.v[e] = hg * sigmoidf_(hg) * hu;
-                }
-                const Enc16 q8 = quantize_block16(av);
-                if (ok) {
-#pragma unroll
-                    for (int g4 = 0; g4 < 4; ++g4)
-                        *reinterpret_cast<uint32_t *>(el + ib + g4 * 8 + (lane >> 5) * 4) = q8.enc[g4];
-                    if (lane < 32) sc[ib / 32] = (uint8_t)q8.scale;
-                }
+            for (int e = 0; e < 16; ++e) {
+                const float hg = acc[fm][0][e], hu = acc[fm][1][e];
+                av.v[e] = hg * sigmoidf_(hg) * hu;
             }
+            const Enc16 q8 = encode_block16(av);
+#pragma unroll
+            for (int g4 = 0; g4 < 4; ++g4) put4(area + code_off<FS>(lane & 31, g4, lane), q8.enc[g4]);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {   // 16 rows a pass, 8 codes a lane
+                const int r = p * 16 + (lane >> 2);
+                bstore8_nt(qres, (m0 + (uint32_t)r) * (uint32_t)I + (uint32_t)(ib0 + (lane & 3) * 8), 0,
+                           FS::get(area + FS::at(r, lane & 3)));
+            }
+            bstore1(sres, lane < 32 ? (m0 + (uint32_t)lane) * (uint32_t)(I / 32) + (uint32_t)(ib0 / 32) : kOutOfRange,
+                    q8.scale);
         }
     }
 };
@@ -149,8 +169,15 @@ struct FfnDA8 : Ffn8Base {
         sl.init(x_scales(H, k0), t.rows, H / 32, a.w0s + (int64_t)i0 * (H / 32) + k0 / 32, nw, H / 32);
         return true;
     }
+    // As the BF16 dA: h rows come in and dh and a rows leave as whole row runs,
+    // staged one 32-row fragment at a time through row descriptors; dh's codes
+    // take a fourth staging array, their scales one 2-byte store a row and half.
+    // (Storing each lane's pieces directly and quantizing out of line, every
+    // call waiting for all stores in flight, the kernel took 411 us at
+    // 16,384 x 7,168 x 2,048.)
     __device__ void epilogue(f32x16_t (&acc)[C::FM][C::FN], int wm, int wn) {
-        const int lane = threadIdx.x & 63;
+        using FS = FragStage<C, S8::LDS_BYTES>;
+        static_assert(C::FN == 2 && S8::LDS_BYTES >= 4 * (size_t)C::NW * FS::BYTES, "four staged arrays");
         const int I = a.I, ib0 = t.nt * C::BN + wn * C::WN;
         const bool live = ib0 < I;   // I % 128 == 0: a wave's 64 columns are all valid or none
         if (a.splits > 1) {
@@ -158,51 +185,82 @@ struct FfnDA8 : Ffn8Base {
                               [&](int fn) { return ib0 + fn * 32; });
             return;
         }
-        if (!live) return;
+        const int lane = epi_lane();
+        const int ib = live ? ib0 : 0;
+        const uint32_t rows = live ? (uint32_t)t.rows : 0u;
+        const uint32_t sg = FS::area(wave_id(), 4), su = sg + FS::BYTES, sa = su + FS::BYTES, sq = sa + FS::BYTES;
+        const uint32_t up = 2u * (uint32_t)I, row_bytes = 2u * up, sc_bytes = up / 32;
+        const brsrc_t hres = rows_rsrc(a.h_in + (int64_t)t.m0 * 2 * I, rows * row_bytes);
+        const brsrc_t dres = rows_rsrc(a.dh + (int64_t)t.m0 * 2 * I, rows * row_bytes);
+        const brsrc_t ares = rows_rsrc(a.a + (int64_t)t.m0 * I, rows * up);
+        const brsrc_t qres = rows_rsrc(a.q + (int64_t)t.m0 * 2 * I, rows * up);
+        const brsrc_t sres = rows_rsrc(a.qs + (int64_t)t.m0 * sc_bytes, rows * sc_bytes);
+        // the lane's byte offsets at pass 0 of fragment 0; pass p of fragment fm lies step(fm, p) rows further.
+        // A row's 128 staged code bytes are 64 of the gate half and 64 of the up half.
+        const uint32_t row0 = (uint32_t)(wm * C::WM + FS::pass_row(0, lane));
+        const uint32_t d0 = row0 * row_bytes + 2u * (uint32_t)(ib + FS::pass_col(lane));
+        const uint32_t a0 = row0 * up + 2u * (uint32_t)(ib + FS::pass_col(lane));
+        const uint32_t q0 = row0 * up + (uint32_t)(ib + (lane % 8) * 8 + (lane % 16 >= 8 ? I : 0));
+        auto step = [](int fm, int p) { return (uint32_t)(fm * 32 + p * FS::RPP); };
+        uint2 hg[FS::PASSES], hu[FS::PASSES];
+        auto load_h = [&](int fm) {
+#pragma unroll
+            for (int p = 0; p < FS::PASSES; ++p) {
+                hg[p] = bload8(hres, d0 + step(fm, p) * row_bytes, 0);
+                hu[p] = bload8(hres, d0 + step(fm, p) * row_bytes, up);
+            }
+        };
+        load_h(0);
 #pragma unroll
         for (int fm = 0; fm < C::FM; ++fm) {
-            const int m = wm * C::WM + fm * 32 + (lane & 31);
-            const bool ok = m < t.rows;
-            const int64_t r = t.m0 + (ok ? m : 0);
-            HBatch<C> h;
-            h.load(a.h_in + r * 2 * I, I, ib0, lane);
-            uint16_t *dhrow = a.dh + r * 2 * I, *arow = a.a + r * I;
-            uint8_t *qrow = a.q + r * 2 * I, *srow = a.qs + r * (2 * I / 32);
+#pragma unroll
+            for (int p = 0; p < FS::PASSES; ++p) {
+                FS::put(sg + FS::pass_off(p, lane), hg[p]);
+                FS::put(su + FS::pass_off(p, lane), hu[p]);
+            }
+            __builtin_amdgcn_sched_barrier(0);   // phases stay in order: keeps live ranges short
+            uint32_t sc = 0;   // lanes below 32: the gate half's two scale bytes of row lane, the others: the up half's
 #pragma unroll
             for (int fn = 0; fn < C::FN; ++fn) {
-                const int ib = ib0 + fn * 32;   // one 32-block of i
                 Block16 dg, du;
 #pragma unroll
                 for (int g4 = 0; g4 < 4; ++g4) {
-                    const int i = ib + g4 * 8 + (lane >> 5) * 4, e = g4 * 4;
+                    const uint32_t o = FS::frag_off(fn, g4, lane);
+                    const int e = g4 * 4;
+                    const uint2 hg2 = FS::get(sg + o), hu2 = FS::get(su + o);
                     float av[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const GluGrad g = glu_backward(acc[fm][fn][e + j], bf16_at(h.g[fn][g4], j), bf16_at(h.u[fn][g4], j));
+                        const GluGrad g = glu_backward(acc[fm][fn][e + j], bf16_at(hg2, j), bf16_at(hu2, j));
                         av[j] = g.a;
                         dg.v[e + j] = g.dg;
                         du.v[e + j] = g.du;
                     }
-                    if (ok) {
-                        store4_bf16(arow + i, av[0], av[1], av[2], av[3]);
-                        store4_bf16(dhrow + i, dg.v[e], dg.v[e + 1], dg.v[e + 2], dg.v[e + 3]);
-                        store4_bf16(dhrow + I + i, du.v[e], du.v[e + 1], du.v[e + 2], du.v[e + 3]);
-                    }
+                    FS::put(sg + o, make_uint2(pack_bf16x2(dg.v[e], dg.v[e + 1]), pack_bf16x2(dg.v[e + 2], dg.v[e + 3])));
+                    FS::put(su + o, make_uint2(pack_bf16x2(du.v[e], du.v[e + 1]), pack_bf16x2(du.v[e + 2], du.v[e + 3])));
+                    FS::put(sa + o, make_uint2(pack_bf16x2(av[0], av[1]), pack_bf16x2(av[2], av[3])));
                 }
-                const Enc16 qg = quantize_block16(dg), qu = quantize_block16(du);
-                if (ok) {
+                const Enc16 qg = encode_block16(dg), qu = encode_block16(du);
 #pragma unroll
-                    for (int g4 = 0; g4 < 4; ++g4) {
-                        const int i = ib + g4 * 8 + (lane >> 5) * 4;
-                        *reinterpret_cast<uint32_t *>(qrow + i) = qg.enc[g4];
-                        *reinterpret_cast<uint32_t *>(qrow + I + i) = qu.enc[g4];
-                    }
-                    if (lane < 32) {
-                        srow[ib / 32] = (uint8_t)qg.scale;
-                        srow[(I + ib) / 32] = (uint8_t)qu.scale;
-                    }
+                for (int g4 = 0; g4 < 4; ++g4) {
+                    put4(sq + code_off<FS>(lane & 31, fn * 4 + g4, lane), qg.enc[g4]);
+                    put4(sq + code_off<FS>(lane & 31, 8 + fn * 4 + g4, lane), qu.enc[g4]);
                 }
+                sc |= (lane < 32 ? qg.scale : qu.scale) << (8 * fn);
+                __builtin_amdgcn_sched_barrier(0);
             }
+            if (fm + 1 < C::FM) load_h(fm + 1);   // in flight while this fragment's rows are stored
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int p = 0; p < FS::PASSES; ++p) {
+                const uint32_t o = FS::pass_off(p, lane), v = d0 + step(fm, p) * row_bytes;
+                bstore8_nt(dres, v, 0, FS::get(sg + o));
+                bstore8_nt(dres, v, up, FS::get(su + o));
+                bstore8_nt(ares, a0 + step(fm, p) * up, 0, FS::get(sa + o));
+                bstore8_nt(qres, q0 + step(fm, p) * up, 0, FS::get(sq + o));
+            }
+            const uint32_t sr = (uint32_t)(wm * C::WM + fm * 32 + (lane & 31)) * sc_bytes;
+            bstore2(sres, sr + (uint32_t)((ib + (lane < 32 ? 0 : I)) / 32), sc);
         }
     }
 };

@@ -190,11 +190,22 @@ inline unsigned wgrad_grid(int M, int N, int bm) {
 
 // ----------------------------------------------------------------------------- joining partials
 
-// Sum of the runs' partials of 4 consecutive columns, in ascending order.
+// Sum of the runs' partials of 4 consecutive columns, in ascending order. A
+// join of few rows is bound by the latency of these loads (each was written by
+// another XCD, so none hits in L2): 8 are in flight before the first is added.
+// Runs past the last are loaded again and left out of the sum.
+constexpr int kJoinBatch = 8;
 __device__ __forceinline__ f32x4_t sum_runs(const float *part, int64_t stride, int splits) {
-    f32x4_t s = *reinterpret_cast<const f32x4_t *>(part);
-#pragma unroll 4
-    for (int i = 1; i < splits; ++i) s += *reinterpret_cast<const f32x4_t *>(part + i * stride);
+    f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i0 = 0; i0 < splits; i0 += kJoinBatch) {
+        f32x4_t v[kJoinBatch];
+#pragma unroll
+        for (int j = 0; j < kJoinBatch; ++j)
+            v[j] = *reinterpret_cast<const f32x4_t *>(part + min(i0 + j, splits - 1) * stride);
+#pragma unroll
+        for (int j = 0; j < kJoinBatch; ++j)
+            if (i0 + j < splits) s += v[j];
+    }
     return s;
 }
 
@@ -217,9 +228,8 @@ template <bool MX>
 __global__ __launch_bounds__(256) void ffn_join_act(const float *__restrict__ part, int splits, int T, int I,
                                                     uint16_t *__restrict__ h, uint16_t *__restrict__ a,
                                                     uint8_t *__restrict__ aq, uint8_t *__restrict__ aqs) {
-    const int per = I / 4;
-    const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (idx >= (int64_t)T * per) return;   // whole groups of 8 lanes: I / 4 is a multiple of 8
+    const uint32_t per = (uint32_t)I / 4, idx = blockIdx.x * 256u + threadIdx.x;   // T * I < 2^29
+    if (idx >= (uint32_t)T * per) return;   // whole groups of 8 lanes: I / 4 is a multiple of 8
     const int64_t t = idx / per;
     const int i = (int)(idx % per) * 4;
     const int64_t stride = (int64_t)T * 2 * I;
@@ -246,9 +256,8 @@ __global__ __launch_bounds__(256) void ffn_join_act(const float *__restrict__ pa
 // out = addend + sum of the partials. out and addend may be one buffer.
 __global__ __launch_bounds__(256) void ffn_join_out(const float *__restrict__ part, int splits, int T, int N,
                                                     const uint16_t *addend, uint16_t *out) {
-    const int per = N / 4;
     const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (idx >= (int64_t)T * per) return;
+    if (idx >= (int64_t)T * (N / 4)) return;
     uint2 b = make_uint2(0, 0);
     if (addend) b = reinterpret_cast<const uint2 *>(addend)[idx];
     const f32x4_t s = sum_runs(part + idx * 4, (int64_t)T * N, splits);
@@ -271,9 +280,8 @@ __global__ __launch_bounds__(256) void ffn_join_da(const float *__restrict__ par
                                                    const uint16_t *__restrict__ h, uint16_t *__restrict__ dh,
                                                    uint16_t *__restrict__ a, uint8_t *__restrict__ dhq,
                                                    uint8_t *__restrict__ dhqs) {
-    const int per = I / 4;
-    const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (idx >= (int64_t)T * per) return;
+    const uint32_t per = (uint32_t)I / 4, idx = blockIdx.x * 256u + threadIdx.x;
+    if (idx >= (uint32_t)T * per) return;
     const int64_t t = idx / per;
     const int i = (int)(idx % per) * 4;
     const int64_t row = t * 2 * I;

@@ -72,9 +72,9 @@ struct NormBackwardCall {
     void *dres;
     uint16_t *dx;
     float *dweight;
-    float *part;   // norm_backward_blocks(T) x H floats
+    float *part;   // norm_backward_shares(T, H) x H floats
 };
-int norm_backward_blocks(int64_t T);
+int64_t norm_backward_shares(int64_t T, int H);
 mok_status launch_add_rmsnorm_backward(const NormBackwardCall &c, hipStream_t st);
 
 struct FfnPlan;

@@ -10,8 +10,10 @@ namespace {
 // l ^ 32 holds the other 16, columns g4*8 + 4*(l/32) + j of the block).
 // Returns the scale byte and, in enc[g4], the 4 codes of columns
 // g4*8 + 4h .. +3. Every lane of the wave must call this (cross-lane
-// exchange). Kept out of line: epilogues call it up to 16 times, and inlining
-// every copy would stop the accumulator loops from unrolling.
+// exchange). quantize_block16 is kept out of line: epilogues call it up to 16
+// times, and inlining every copy would stop the accumulator loops from
+// unrolling. A call waits for every load and store in flight, though; an
+// epilogue that keeps stores in flight uses encode_block16.
 struct Block16 {
     float v[16];
 };
@@ -19,7 +21,7 @@ struct Enc16 {
     uint32_t enc[4];
     uint32_t scale;
 };
-__device__ __attribute__((noinline)) Enc16 quantize_block16(Block16 b) {
+__device__ __forceinline__ Enc16 encode_block16(const Block16 &b) {
     uint32_t amax = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(b.v[i]) & 0x7FFFFFFFu);
@@ -33,6 +35,7 @@ __device__ __attribute__((noinline)) Enc16 quantize_block16(Block16 b) {
                     (e4m3x2_scaled(b.v[g4 * 4 + 2] * sc, b.v[g4 * 4 + 3] * sc) << 16);
     return r;
 }
+__device__ __attribute__((noinline)) Enc16 quantize_block16(Block16 b) { return encode_block16(b); }
 
 }  // namespace
 }  // namespace mok
