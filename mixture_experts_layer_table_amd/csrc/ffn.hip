@@ -20,7 +20,10 @@ namespace {
 
 using CfgA = TileCfg<256, 256, 2, 4, 4>;   // as the layer's: 4 stages of 32 KiB
 using CfgS = TileCfg<128, 256, 2, 4, 6>;   // 6 stages of 24 KiB
-static_assert(CfgA::BN == kTileN && CfgS::BN == kTileN, "host sizing assumes kTileN-column tiles");
+// CfgS at half the LDS and at most 128 registers: two workgroups per compute
+// unit, one's stores beside the other's loads
+using CfgW = TileCfg<128, 256, 2, 4, 3, 4>;
+static_assert(CfgA::BN == kTileN && CfgS::BN == kTileN && CfgW::BN == kTileN, "host sizing assumes kTileN-column tiles");
 
 struct FfnArgs {
     int T, H, I, n_tiles, splits, len;
@@ -291,7 +294,7 @@ __global__ __launch_bounds__(P::C::NT, P::C::OCC) void ffn_gemm(typename P::Args
 // dW_gate | dW_up, dW_down and dx in one launch, the weight gradients (the
 // longer K loops) first; g0, g1: workgroups of the first two.
 template <class PX, class PW>
-__global__ __launch_bounds__(PX::C::NT, 2) void ffn_grads(typename PW::Args gu, typename PW::Args wd,
+__global__ __launch_bounds__(PX::C::NT, PX::C::OCC) void ffn_grads(typename PW::Args gu, typename PW::Args wd,
                                                           typename PX::Args ax, int g0, int g1) {
     extern __shared__ __attribute__((aligned(1024))) char lds_raw[];
     const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds_raw;
@@ -405,8 +408,15 @@ hipError_t backward_bf16(const FfnPlan &p, char *ws, const uint16_t *x, const mo
     a.len = p.dx.len;
     const FfnWgradArgs gu{a.T, p.H, 2 * p.I, p.I, p.I, x, a.dh, dw_gate, dw_up};
     const FfnWgradArgs wd{a.T, p.I, p.H, p.H, p.H, a.a, dy, dw_down, nullptr};
-    if (p.dx.bm == CfgS::BM)
-        e = p.wgrad_bm == CfgS::BM ? launch_grads<CfgS, CfgS>(gu, wd, a, st) : launch_grads<CfgS, CfgA>(gu, wd, a, st);
+    if (p.dx.bm == CfgS::BM && p.wgrad_bm == CfgS::BM) {
+        // with more tiles than compute units, two workgroups a unit (1,001 and
+        // 2,048 rows of 4,096 x 1,024: backward 84 -> 78 and 142 -> 131 us);
+        // with fewer, the deeper ring (2,048 rows of 1,024 x 512: 60 us against 71)
+        const int64_t tiles = wgrad_grid(gu.M, gu.N, CfgS::BM) + wgrad_grid(wd.M, wd.N, CfgS::BM) +
+                              ffn_grid(p.T, CfgS::BM, a.n_tiles, a.splits);
+        e = tiles > 256 ? launch_grads<CfgW, CfgW>(gu, wd, a, st) : launch_grads<CfgS, CfgS>(gu, wd, a, st);
+    } else if (p.dx.bm == CfgS::BM)
+        e = launch_grads<CfgS, CfgA>(gu, wd, a, st);
     else
         e = p.wgrad_bm == CfgS::BM ? launch_grads<CfgA, CfgS>(gu, wd, a, st) : launch_grads<CfgA, CfgA>(gu, wd, a, st);
     if (e == hipSuccess && p.T > 0 && p.dx.splits > 1) {

@@ -16,8 +16,10 @@ namespace mok {
 namespace {
 
 using CfgA = TileCfg<256, 256, 2, 4, 4>;
-using CfgS = TileCfg<128, 256, 2, 4, 6>;
-using S8 = Fp8Stage<CfgA>;
+using CfgH = TileCfg<128, 256, 2, 4, 4>;   // half the rows: twice the tiles before a product has to be split
+using CfgS = TileCfg<128, 256, 2, 4, 6>;   // BF16 weight gradients
+constexpr int kK8 = 64;                    // fp8 values per row and stage
+static_assert(Fp8Stage<CfgA>::BK8 == kK8 && Fp8Stage<CfgH>::BK8 == kK8, "one K-step for both tiles");
 
 __device__ __forceinline__ const uint16_t *as_pairs(const uint8_t *p) { return reinterpret_cast<const uint16_t *>(p); }
 
@@ -48,9 +50,12 @@ struct Ffn8Args {
 };
 
 // Members that every problem below shares: loaders, tile and K-step issue.
+template <class Cfg>
 struct Ffn8Base {
-    using C = CfgA;
+    using C = Cfg;
+    using S8 = Fp8Stage<C>;
     using Args = Ffn8Args;
+    static constexpr size_t LDS = S8::LDS_BYTES;   // dynamic LDS of the launch
     RowLoader<C, C::BM> xl;
     RowLoader<C, C::BN> wl;
     ScaleLoader<C> sl;
@@ -63,8 +68,8 @@ struct Ffn8Base {
     __device__ bool begin(const Args &args, int b, int K, int &k0) {
         a = args;
         if (!ffn_tile(a.T, C::BM, a.n_tiles, a.splits, b, t)) return false;
-        k0 = t.s * a.len * S8::BK8;
-        nk = min(a.len, K / S8::BK8 - t.s * a.len);
+        k0 = t.s * a.len * kK8;
+        nk = min(a.len, K / kK8 - t.s * a.len);
         xl.init(as_pairs(a.x + (int64_t)t.m0 * K + k0), K / 2, t.rows);
         return true;
     }
@@ -77,7 +82,19 @@ struct Ffn8Base {
     __device__ int wrow(int wn, int fn) const { return wn * C::WN + fn * 32; }
 };
 
-struct FfnGateUp8 : Ffn8Base {
+template <class Cfg>
+struct FfnGateUp8 : Ffn8Base<Cfg> {
+    using B = Ffn8Base<Cfg>;
+    using typename B::Args;
+    using typename B::C;
+    using typename B::S8;
+    using B::a;
+    using B::begin;
+    using B::sl;
+    using B::t;
+    using B::wl;
+    using B::xl;
+    using B::x_scales;
     __device__ bool setup(const Args &args, int b) {
         int k0;
         const int H = args.H;
@@ -144,7 +161,19 @@ struct FfnGateUp8 : Ffn8Base {
     }
 };
 
-struct FfnDown8 : Ffn8Base {
+template <class Cfg>
+struct FfnDown8 : Ffn8Base<Cfg> {
+    using B = Ffn8Base<Cfg>;
+    using typename B::Args;
+    using typename B::C;
+    using typename B::S8;
+    using B::a;
+    using B::begin;
+    using B::sl;
+    using B::t;
+    using B::wl;
+    using B::xl;
+    using B::x_scales;
     __device__ bool setup(const Args &args, int b) {
         int k0;
         const int I = args.I;
@@ -159,7 +188,19 @@ struct FfnDown8 : Ffn8Base {
     }
 };
 
-struct FfnDA8 : Ffn8Base {
+template <class Cfg>
+struct FfnDA8 : Ffn8Base<Cfg> {
+    using B = Ffn8Base<Cfg>;
+    using typename B::Args;
+    using typename B::C;
+    using typename B::S8;
+    using B::a;
+    using B::begin;
+    using B::sl;
+    using B::t;
+    using B::wl;
+    using B::xl;
+    using B::x_scales;
     __device__ bool setup(const Args &args, int b) {
         int k0;
         const int H = args.H;
@@ -169,6 +210,8 @@ struct FfnDA8 : Ffn8Base {
         sl.init(x_scales(H, k0), t.rows, H / 32, a.w0s + (int64_t)i0 * (H / 32) + k0 / 32, nw, H / 32);
         return true;
     }
+    // four staged arrays of 4 KiB a wave, which may be more than the tile's own LDS
+    static constexpr size_t LDS = S8::LDS_BYTES > 4 * (size_t)C::NW * 4096 ? S8::LDS_BYTES : 4 * (size_t)C::NW * 4096;
     // As the BF16 dA: h rows come in and dh and a rows leave as whole row runs,
     // staged one 32-row fragment at a time through row descriptors; dh's codes
     // take a fourth staging array, their scales one 2-byte store a row and half.
@@ -176,8 +219,8 @@ struct FfnDA8 : Ffn8Base {
     // call waiting for all stores in flight, the kernel took 411 us at
     // 16,384 x 7,168 x 2,048.)
     __device__ void epilogue(f32x16_t (&acc)[C::FM][C::FN], int wm, int wn) {
-        using FS = FragStage<C, S8::LDS_BYTES>;
-        static_assert(C::FN == 2 && S8::LDS_BYTES >= 4 * (size_t)C::NW * FS::BYTES, "four staged arrays");
+        using FS = FragStage<C, LDS>;
+        static_assert(C::FN == 2 && LDS >= 4 * (size_t)C::NW * FS::BYTES, "four staged arrays");
         const int I = a.I, ib0 = t.nt * C::BN + wn * C::WN;
         const bool live = ib0 < I;   // I % 128 == 0: a wave's 64 columns are all valid or none
         if (a.splits > 1) {
@@ -265,7 +308,19 @@ struct FfnDA8 : Ffn8Base {
     }
 };
 
-struct FfnDX8 : Ffn8Base {
+template <class Cfg>
+struct FfnDX8 : Ffn8Base<Cfg> {
+    using B = Ffn8Base<Cfg>;
+    using typename B::Args;
+    using typename B::C;
+    using typename B::S8;
+    using B::a;
+    using B::begin;
+    using B::sl;
+    using B::t;
+    using B::wl;
+    using B::xl;
+    using B::x_scales;
     __device__ bool setup(const Args &args, int b) {
         int k0;
         const int I = args.I;
@@ -306,7 +361,7 @@ __global__ __launch_bounds__(256) void ffn_quantize_rows(const uint16_t *__restr
 }
 
 template <class P>
-__global__ __launch_bounds__(CfgA::NT, 2) void ffn_gemm8(Ffn8Args args) {
+__global__ __launch_bounds__(P::C::NT, 2) void ffn_gemm8(Ffn8Args args) {
     extern __shared__ __attribute__((aligned(1024))) char lds_raw[];
     P p;
     if (!p.setup(args, (int)blockIdx.x)) return;
@@ -314,8 +369,8 @@ __global__ __launch_bounds__(CfgA::NT, 2) void ffn_gemm8(Ffn8Args args) {
 }
 
 // dW_gate | dW_up and dW_down (BF16 tiles), then dx (block-scaled tiles), in one launch.
-template <class PW>
-__global__ __launch_bounds__(CfgA::NT, 2) void ffn_grads8(FfnWgradArgs gu, FfnWgradArgs wd, Ffn8Args ax, int g0, int g1) {
+template <class PX, class PW>
+__global__ __launch_bounds__(PX::C::NT, 2) void ffn_grads8(FfnWgradArgs gu, FfnWgradArgs wd, Ffn8Args ax, int g0, int g1) {
     extern __shared__ __attribute__((aligned(1024))) char lds_raw[];
     const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds_raw;
     int b = (int)blockIdx.x;
@@ -324,36 +379,43 @@ __global__ __launch_bounds__(CfgA::NT, 2) void ffn_grads8(FfnWgradArgs gu, FfnWg
         if (!p.setup(b < g0 ? gu : wd, b < g0 ? b : b - g0)) return;
         gemm_tile(p, lds);
     } else {
-        FfnDX8 p;
+        PX p;
         if (!p.setup(ax, b - g0 - g1)) return;
         gemm8_tile(p, lds);
     }
 }
 
 template <class P>
-hipError_t product8(const char *name, const FfnSplit &s, Ffn8Args a, int n_tiles, hipStream_t st) {
+hipError_t launch_product8(const char *name, unsigned grid, const Ffn8Args &a, hipStream_t st) {
     static std::atomic<uint64_t> done{0};
-    const hipError_t e = allow_lds(ffn_gemm8<P>, S8::LDS_BYTES, done);
+    const hipError_t e = allow_lds(ffn_gemm8<P>, P::LDS, done);
     if (e != hipSuccess) return e;
-    a.n_tiles = n_tiles;
-    a.splits = s.splits;
-    a.len = s.len;
     KernelTimer tm(name, st);
-    ffn_gemm8<P><<<ffn_grid(a.T, s.bm, n_tiles, s.splits), CfgA::NT, S8::LDS_BYTES, st>>>(a);
+    ffn_gemm8<P><<<grid, P::C::NT, P::LDS, st>>>(a);
     return hipGetLastError();
 }
 
-template <class CW>
+template <template <class> class P>
+hipError_t product8(const char *name, const FfnSplit &s, Ffn8Args a, int n_tiles, hipStream_t st) {
+    a.n_tiles = n_tiles;
+    a.splits = s.splits;
+    a.len = s.len;
+    const unsigned grid = ffn_grid(a.T, s.bm, n_tiles, s.splits);
+    return s.bm == CfgH::BM ? launch_product8<P<CfgH>>(name, grid, a, st) : launch_product8<P<CfgA>>(name, grid, a, st);
+}
+
+template <class CX, class CW>
 hipError_t launch_grads8(const FfnWgradArgs &gu, const FfnWgradArgs &wd, const Ffn8Args &ax, hipStream_t st) {
+    using PX = FfnDX8<CX>;
     static std::atomic<uint64_t> done{0};
-    auto *k = ffn_grads8<FfnWgrad<CW>>;
-    constexpr size_t lds = S8::LDS_BYTES > CW::LDS_BYTES ? S8::LDS_BYTES : CW::LDS_BYTES;
+    auto *k = ffn_grads8<PX, FfnWgrad<CW>>;
+    constexpr size_t lds = PX::LDS > CW::LDS_BYTES ? PX::LDS : CW::LDS_BYTES;
     const hipError_t e = allow_lds(k, lds, done);
     if (e != hipSuccess) return e;
     const unsigned g0 = wgrad_grid(gu.M, gu.N, CW::BM), g1 = wgrad_grid(wd.M, wd.N, CW::BM);
-    const unsigned gx = ffn_grid(ax.T, CfgA::BM, ax.n_tiles, ax.splits);
+    const unsigned gx = ffn_grid(ax.T, CX::BM, ax.n_tiles, ax.splits);
     KernelTimer tm("ffn_grads_mx", st);
-    k<<<g0 + g1 + gx, CfgA::NT, lds, st>>>(gu, wd, ax, (int)g0, (int)g1);
+    k<<<g0 + g1 + gx, CX::NT, lds, st>>>(gu, wd, ax, (int)g0, (int)g1);
     return hipGetLastError();
 }
 
@@ -441,7 +503,10 @@ hipError_t ffn_mx_backward(const FfnPlan &p, char *ws, const uint16_t *x, const 
     a.len = p.dx.len;
     const FfnWgradArgs gu{a.T, p.H, 2 * p.I, p.I, p.I, x, a.dh, dw_gate, dw_up};
     const FfnWgradArgs wd{a.T, p.I, p.H, p.H, p.H, a.a, dy, dw_down, nullptr};
-    e = p.wgrad_bm == CfgS::BM ? launch_grads8<CfgS>(gu, wd, a, st) : launch_grads8<CfgA>(gu, wd, a, st);
+    if (p.dx.bm == CfgH::BM)
+        e = p.wgrad_bm == CfgS::BM ? launch_grads8<CfgH, CfgS>(gu, wd, a, st) : launch_grads8<CfgH, CfgA>(gu, wd, a, st);
+    else
+        e = p.wgrad_bm == CfgS::BM ? launch_grads8<CfgA, CfgS>(gu, wd, a, st) : launch_grads8<CfgA, CfgA>(gu, wd, a, st);
     if (e == hipSuccess && p.T > 0 && p.dx.splits > 1) {
         KernelTimer tm("ffn_join_out", st);
         ffn_join_out<<<join_grid(p.T, p.H), 256, 0, st>>>(a.part, p.dx.splits, a.T, a.H, addend, dx);

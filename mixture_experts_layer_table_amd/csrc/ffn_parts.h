@@ -84,14 +84,16 @@ __device__ __forceinline__ void store_rows_add(const f32x16_t (&acc)[C::FM][C::F
     using FS = FragStage<C, LDS_END>;
     const int lane = epi_lane();
     const uint32_t area = FS::area(wave_id(), 1);
-    auto voff = [&](int fm, int p) {
-        return (uint32_t)(wm * C::WM + fm * 32 + FS::pass_row(p, lane)) * row_bytes + 2u * (uint32_t)FS::pass_col(lane);
-    };
-#pragma unroll
-    for (int fm = 0; fm < C::FM; ++fm) {
-        uint2 ad[FS::PASSES];
+    const uint32_t v0 = (uint32_t)(wm * C::WM + FS::pass_row(0, lane)) * row_bytes + 2u * (uint32_t)FS::pass_col(lane);
+    auto voff = [&](int fm, int p) { return v0 + (uint32_t)(fm * 32 + p * FS::RPP) * row_bytes; };
+    uint2 ad[FS::PASSES];
+    auto load = [&](int fm) {
 #pragma unroll
         for (int p = 0; p < FS::PASSES; ++p) ad[p] = bload8(add, voff(fm, p), 0);
+    };
+    load(0);
+#pragma unroll
+    for (int fm = 0; fm < C::FM; ++fm) {
 #pragma unroll
         for (int p = 0; p < FS::PASSES; ++p) FS::put(area + FS::pass_off(p, lane), ad[p]);
         __builtin_amdgcn_sched_barrier(0);   // phases stay in order: keeps live ranges short
@@ -106,6 +108,8 @@ __device__ __forceinline__ void store_rows_add(const f32x16_t (&acc)[C::FM][C::F
                 for (int j = 0; j < 4; ++j) y[j] = acc[fm][fn][g4 * 4 + j] + bf16_at(b, j);
                 FS::put(o, make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])));
             }
+        __builtin_amdgcn_sched_barrier(0);
+        if (fm + 1 < C::FM) load(fm + 1);   // ahead of this fragment's stores: other rows, so also in place
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int p = 0; p < FS::PASSES; ++p) bstore8_nt(dst, voff(fm, p), 0, FS::get(area + FS::pass_off(p, lane)));
@@ -127,8 +131,12 @@ __device__ __forceinline__ void dense_epilogue(const f32x16_t (&acc)[C::FM][C::F
     const uint32_t row_bytes = 2u * (uint32_t)N;
     const int64_t o = (int64_t)t.m0 * N + (live ? nb : 0);
     const uint32_t bytes = live ? (uint32_t)t.rows * row_bytes : 0u;
-    store_rows_add<C, LDS_END>(acc, wm, rows_rsrc(out + o, bytes), rows_rsrc(addend ? addend + o : out, addend ? bytes : 0u),
-                               row_bytes);
+    const brsrc_t dst = rows_rsrc(out + o, bytes);
+    if (addend)
+        store_rows_add<C, LDS_END>(acc, wm, dst, rows_rsrc(addend + o, bytes), row_bytes);
+    else
+        staged_rows<C, LDS_END>([&](int fm, int fn, int g4, int j) { return acc[fm][fn][g4 * 4 + j]; }, dst,
+                                [&](int fm, int r) -> uint32_t { return (uint32_t)(wm * C::WM + fm * 32 + r) * row_bytes; });
 }
 
 // ----------------------------------------------------------------------------- weight gradients

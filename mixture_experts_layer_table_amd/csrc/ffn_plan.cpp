@@ -39,8 +39,7 @@ FfnSplit choose(int64_t T, int64_t N, int64_t n_tiles, int steps, bool mx) {
     FfnSplit best{256, 1, steps};
     double least = 1e30;
     for (int bm : {256, 128}) {
-        if (mx && bm != 256) continue;   // the block-scaled tile is 256 x 256
-        const double step_us = mx ? 0.9 : bm == 256 ? 0.85 : 0.5;
+        const double step_us = bm == 256 ? (mx ? 0.9 : 0.85) : (mx ? 0.55 : 0.5);
         for (int s = 1; s <= kMaxSplits; ++s) {
             int len = (int)ceil_div(steps, s);
             if (mx) len = (len + 1) / 2 * 2;   // whole 128-value runs: one dword of scales a row
