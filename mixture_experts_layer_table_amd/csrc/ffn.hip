@@ -8,10 +8,12 @@
 // holds matching gate and up columns, and its epilogue writes a (and the saved
 // h). The tiles are the library's BF16 tile engine (gemm.h).
 //
-// Few rows leave most compute units without a tile, so a product is then cut
+// A few rows (ffn_few.hip) take kernels of their own. Somewhat more still leave
+// most compute units without a tile, so a product is then cut
 // along its contraction axis (ffn_plan.cpp) and its fp32 partials are added by
 // a second, elementwise kernel that also does the epilogue's work. The weight
 // gradients and dx all wait for dh alone and run as one launch.
+#include "ffn_few.h"
 #include "ffn_parts.h"
 #include "kernels.h"
 
@@ -439,8 +441,13 @@ mok_status launch_ffn_forward(const FfnPlan &p, void *workspace, const uint16_t 
                               const uint8_t *x_scales, const mok_weights &w, const uint16_t *addend, uint16_t *out,
                               uint16_t *h, hipStream_t st) {
     char *ws = static_cast<char *>(workspace);
-    const hipError_t e = p.mx ? ffn_mx_forward(p, ws, x_elems, x_scales, w, addend, out, h, st)
-                              : forward_bf16(p, ws, x, w, addend, out, h, st);
+    hipError_t e;
+    if (p.few_runs)
+        e = p.mx ? ffn_few_mx_forward(p, ws, x_elems, x_scales, w, addend, out, h, st)
+                 : ffn_few_forward(p, ws, x, w, addend, out, h, st);
+    else
+        e = p.mx ? ffn_mx_forward(p, ws, x_elems, x_scales, w, addend, out, h, st)
+                 : forward_bf16(p, ws, x, w, addend, out, h, st);
     return check_hip(e, "mok_ffn_forward");
 }
 

@@ -33,29 +33,53 @@ size_t part_bytes(int64_t T, int H, int I) {
 // The tile height and split of a product of T rows, N columns (n_tiles tiles
 // of them) and `steps` K-steps: the least estimated time over the choices,
 // from the rounds of tiles over the compute units, the time of a K-step, and
-// the traffic of the partials. Depends on the shape alone, so the bits of a
-// result do too.
+// the join with its partials' traffic. The constants were fitted to kernel
+// traces over T from 1 to 4,096 at 7,168 x 2,048, 4,096 x 1,024 and 1,024 x 512
+// (choices 2% slower than the best measured one in the mean, 20% at most).
+// Depends on the shape alone, so the bits of a result do too.
 FfnSplit choose(int64_t T, int64_t N, int64_t n_tiles, int steps, bool mx) {
     FfnSplit best{256, 1, steps};
     double least = 1e30;
     for (int bm : {256, 128}) {
-        const double step_us = bm == 256 ? (mx ? 0.9 : 0.85) : (mx ? 0.55 : 0.5);
+        const double step_us = bm == 256 ? (mx ? 0.9 : 0.85) : (mx ? 0.62 : 0.5);
+        const double tile_us = bm == 256 ? 6.0 : 4.0;
+        const int64_t tiles = ceil_div(T, bm) * n_tiles;
         for (int s = 1; s <= kMaxSplits; ++s) {
             int len = (int)ceil_div(steps, s);
             if (mx) len = (len + 1) / 2 * 2;   // whole 128-value runs: one dword of scales a row
-            const int eff = (int)ceil_div(steps, len);
-            if (s > 1 && (eff != s || len < 4)) continue;
-            if (s > 1 && (size_t)(eff * T * N * 4) > kPartBytes) continue;
-            const int64_t rounds = ceil_div(ceil_div(T, bm) * n_tiles * eff, kUnits);
-            double us = (double)rounds * (len * step_us + 6.0);
-            if (s > 1) us += 5.0 + (double)eff * T * N * 8 / 4.0e6;
+            if (s > 1 && len < 2) break;
+            if (s > 1 && ceil_div(steps, len) != s) continue;
+            if (s > 1 && (size_t)(s * T * N * 4) > kPartBytes) break;
+            double us = (double)ceil_div(tiles * s, kUnits) * (len * step_us + tile_us);
+            if (s > 1) us += 5.5 + 0.1 * s + (double)s * T * N * 8 / 5.0e6;
             if (us < least) {
                 least = us;
-                best = FfnSplit{bm, eff, len};
+                best = FfnSplit{bm, s, len};
             }
         }
     }
     return best;
+}
+
+// The few-rows forward, where it is faster than the tiles (GPU time of a call):
+// one row always (7,168 x 2,048 BF16 26 us against 28, MXFP8 15 against 26;
+// 1,024 x 512 12 against 16 and 7 against 16); two rows in MXFP8 (20 against 26,
+// 10 against 16) and in BF16 up to 2^23 weights a matrix (4,096 x 1,024 19 us
+// against 24; 7,168 x 2,048 32 against 29). Its buffers in LDS stay under
+// 64 KiB (the rows of a in fp32), and BF16 cuts the gate/up product into at
+// most 16 runs of at most 2,048 rows, about one workgroup per compute unit.
+void plan_few(FfnPlan &p) {
+    p.few_runs = p.few_run_rows = 0;
+    if (p.T < 1 || p.T > kFewRows || p.T * p.I > 15 * 1024 || p.H > 16 * 2048) return;
+    if (p.T > 1 && !p.mx && (int64_t)p.H * p.I > (int64_t(1) << 23)) return;
+    p.few_runs = 1;
+    if (p.mx) return;
+    const int64_t strips = p.I / 64, groups = p.H / 64;
+    int64_t runs = std::min<int64_t>(std::max<int64_t>(kUnits / strips, 1), 16);
+    runs = std::max(runs, ceil_div(groups, 2048 / 64));
+    const int64_t len = ceil_div(groups, runs);
+    p.few_run_rows = (int)len * 64;
+    p.few_runs = (int)ceil_div(groups, len);
 }
 
 }  // namespace
@@ -77,6 +101,7 @@ mok_status make_ffn_plan(int64_t T, int32_t H, int32_t I, int32_t precision, Ffn
     p.H = H;
     p.I = I;
     p.mx = mx;
+    plan_few(p);
     const int k = mx ? 64 : 32;
     p.gate_up = choose(T, 2 * (int64_t)I, ceil_div(I, kTileN / 2), H / k, mx);
     p.down = choose(T, H, ceil_div(H, kTileN), I / k, mx);

@@ -16,12 +16,18 @@ struct FfnSplit {
     int bm, splits, len;
 };
 
+// Most rows that take the few-rows kernels (ffn_few.hip).
+constexpr int kFewRows = 2;
+
 struct FfnPlan {
     int64_t T;
     int H, I;
     bool mx;
     FfnSplit gate_up, down, da, dx;
     int wgrad_bm;   // m-tile rows of the weight gradients
+    // few-rows forward: 0 runs where the tile kernels are taken instead;
+    // BF16 gate/up: runs of few_run_rows rows of the weights
+    int few_runs, few_run_rows;
     // workspace offsets (bytes); the forward and the backward overlay each other
     size_t part, a, dh, a_q, a_qs, dh_q, dh_qs, dy_q, dy_qs, total;
 };

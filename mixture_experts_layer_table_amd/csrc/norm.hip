@@ -20,6 +20,7 @@
 #include <type_traits>
 
 #include "kernels.h"
+#include "lanes.h"
 #include "mx_codec.h"
 #include "rng.h"
 #include "timing.h"
@@ -29,18 +30,12 @@ namespace {
 
 constexpr int kMaxWaves = 16;
 
-__device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) x += __shfl_xor(x, off);
-    return x;   // every lane adds the same pairs: all lanes hold the same bits
-}
-
 // Sum over the workgroup in a fixed order; `red` holds one float per wave. One
 // barrier: a caller that sums twice alternates between two buffers, so a wave
 // that runs ahead never overwrites what another still reads.
 __device__ __forceinline__ float block_sum(float x, float *red) {
     const int nw = (int)(blockDim.x >> 6), wave = (int)(threadIdx.x >> 6);
-    x = wave_sum(x);
+    x = sum_wave(x);
     if (nw == 1) return x;
     if ((threadIdx.x & 63) == 0) red[wave] = x;
     __syncthreads();

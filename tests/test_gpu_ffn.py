@@ -25,9 +25,12 @@ TOL_MX = 1e-2
 
 # rows around 1, 32, 128 and 256 (MFMA blocks and tile heights), widths below, at and past one tile, long
 # contraction axes (split) and short ones; BF16 takes multiples of 64, MXFP8 of 128
-SHAPES_BF16 = [(1, 64, 64), (1, 1024, 512), (3, 192, 320), (31, 128, 64), (33, 640, 192), (128, 512, 448),
+# four rows and fewer take kernels of their own: 2 and 4 rows, run lengths and strips that do not divide evenly
+SHAPES_BF16 = [(1, 64, 64), (1, 1024, 512), (3, 192, 320), (2, 320, 192), (4, 2112, 1088), (1, 7168, 2048),
+               (4, 128, 4096), (2, 5120, 64), (31, 128, 64), (33, 640, 192), (128, 512, 448),
                (129, 320, 128), (257, 256, 640), (300, 1088, 576), (700, 64, 1024), (65, 4096, 128), (5, 7168, 2048)]
-SHAPES_MX = [(1, 128, 128), (1, 1024, 512), (3, 256, 384), (31, 128, 256), (33, 640, 256), (257, 256, 640),
+SHAPES_MX = [(1, 128, 128), (1, 1024, 512), (3, 256, 384), (2, 384, 128), (4, 2176, 1152), (1, 7168, 2048),
+             (4, 128, 4096), (2, 5120, 128), (31, 128, 256), (33, 640, 256), (257, 256, 640),
              (300, 1152, 640), (700, 128, 1024), (65, 4096, 128), (5, 7168, 2048)]
 
 
@@ -149,7 +152,7 @@ def test_gradients_are_directional_derivatives():
 
 
 @pytest.mark.parametrize("mx", [False, True])
-@pytest.mark.parametrize("T", [5, 300, 513])
+@pytest.mark.parametrize("T", [1, 3, 5, 300, 513])
 def test_no_h_in_place_and_neighbours_untouched(mx, T):
     H, I = 512, 384
     c = Case(T, H, I, mx, 21)
@@ -173,18 +176,19 @@ def test_no_h_in_place_and_neighbours_untouched(mx, T):
     assert (buf[T:] == 9.0).all()
 
 
-@pytest.mark.parametrize("T", [7, 300])
+@pytest.mark.parametrize("T", [2, 4, 7, 300])
 def test_special_values_stay_in_their_row(T):
     c = Case(T, 256, 192, False, 31)
     out, h = c.forward()
-    c.x[3, 5], c.x[4, 200] = float("nan"), float("inf")
+    a, b = (0, 1) if T == 2 else (1, 3) if T == 4 else (3, 4)
+    c.x[a, 5], c.x[b, 200] = float("nan"), float("inf")
     got, gh = c.forward()
     ok = torch.ones(T, dtype=torch.bool, device=DEV)
-    ok[3:5] = False
+    ok[a] = ok[b] = False
     assert torch.equal(got[ok], out[ok]) and torch.equal(gh[ok], h[ok])
-    assert torch.isnan(got[3]).all()
+    assert torch.isnan(got[a]).all()
     g0 = c.backward(h)["dx"].clone()
-    h[3] = float("nan")
+    h[a] = float("nan")
     assert torch.equal(c.backward(h)["dx"][ok], g0[ok])
 
 
