@@ -62,7 +62,7 @@ FfnSplit choose(int64_t T, int64_t N, int64_t n_tiles, int steps, bool mx) {
 }
 
 // The few-rows forward, where it is faster than the tiles (GPU time of a call):
-// one row always (7,168 x 2,048 BF16 26 us against 28, MXFP8 15 against 26;
+// one row always (7,168 x 2,048 BF16 24 us against 28, MXFP8 14 against 26;
 // 1,024 x 512 12 against 16 and 7 against 16); two rows in MXFP8 (20 against 26,
 // 10 against 16) and in BF16 up to 2^23 weights a matrix (4,096 x 1,024 19 us
 // against 24; 7,168 x 2,048 32 against 29). Its buffers in LDS stay under
