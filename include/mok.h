@@ -364,7 +364,10 @@ mok_status mok_route_backward(const int32_t *topk_ids, const float *topk_w, cons
  *    a captured graph follow the pair's current value. With p == 0 rng is
  *    ignored and may be NULL.
  *  - An output may be the same buffer as an input of the same type and shape
- *    only where a call says so; otherwise buffers must not overlap.
+ *    only where a call says so; otherwise buffers must not overlap (refused).
+ *  - Calls can be captured into a HIP graph once they have run eagerly (kernels
+ *    are loaded and their attributes set on first use). They enqueue kernels
+ *    only. Graphs that share a workspace must not run at the same time.
  */
 #define MOK_STREAM_BF16 0
 #define MOK_STREAM_F32 1
@@ -447,9 +450,9 @@ mok_status mok_add_rmsnorm_backward(const mok_norm_shape *shape, void *workspace
 /*
  * Dense gated feed-forward block (SwiGLU), the shared expert beside the routed
  * ones: T rows of H through an intermediate size I.
- * H and I are multiples of 64 (128 in MXFP8); T >= 0; the layer's bounds on
- * byte offsets hold: T*H*2 < 2^31, T*I*4 < 2^31, (H+256)*I*2 < 2^31 and
- * (I+256)*H*2 < 2^31.
+ * H and I are multiples of 64 (128 in MXFP8), at most 2^20; T >= 0; the
+ * layer's bounds on byte offsets hold: T*H*2 < 2^31, T*I*4 < 2^31,
+ * (H+256)*I*2 < 2^31 and (I+256)*H*2 < 2^31.
  * precision is MOK_BF16 or MOK_MXFP8 (weight gradients in BF16).
  * Weights are a mok_weights for one expert (E = 1), in the orientations that
  * struct describes.
@@ -470,7 +473,7 @@ mok_status mok_ffn_query_size(const mok_ffn_shape *shape, size_t *workspace_byte
  *   x_elems, x_scales   MXFP8: device uint8 [T,H], [T,H/32], the rows quantized
  *             along H (mok_add_rmsnorm or mok_mxfp8_quantize). BF16: NULL
  *   addend    device bf16 [T,H] added to the block's output in fp32 (for
- *             instance mok_forward's out), or NULL
+ *             instance mok_forward's out), or NULL; its gradient is out's
  *   out       device bf16 [T,H]; may be addend's buffer
  *   h         device bf16 [T,2I]: x [W_gate | W_up], which the backward needs,
  *             or NULL

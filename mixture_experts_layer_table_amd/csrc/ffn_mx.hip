@@ -256,6 +256,9 @@ struct FfnDA8 : Ffn8Base<Cfg> {
         load_h(0);
 #pragma unroll
         for (int fm = 0; fm < C::FM; ++fm) {
+            // LDS offsets are worked out anew for each fragment: kept across all
+            // four they spill, and a reload waits behind every store in flight
+            const int lane = epi_lane();
 #pragma unroll
             for (int p = 0; p < FS::PASSES; ++p) {
                 FS::put(sg + FS::pass_off(p, lane), hg[p]);

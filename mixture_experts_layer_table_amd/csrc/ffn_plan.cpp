@@ -41,7 +41,7 @@ FfnSplit choose(int64_t T, int64_t N, int64_t n_tiles, int steps, bool mx) {
     FfnSplit best{256, 1, steps};
     double least = 1e30;
     for (int bm : {256, 128}) {
-        const double step_us = bm == 256 ? (mx ? 0.9 : 0.85) : (mx ? 0.62 : 0.5);
+        const double step_us = bm == 256 ? (mx ? 0.9 : 0.85) : (mx ? 0.74 : 0.5);
         const double tile_us = bm == 256 ? 6.0 : 4.0;
         const int64_t tiles = ceil_div(T, bm) * n_tiles;
         for (int s = 1; s <= kMaxSplits; ++s) {
@@ -90,6 +90,9 @@ mok_status make_ffn_plan(int64_t T, int32_t H, int32_t I, int32_t precision, Ffn
     const bool mx = precision == MOK_MXFP8;
     const int q = mx ? 128 : 64;
     if (H % q || I % q) return MOK_ERROR_INVALID_VALUE;
+    // 256 rows of a tile at 8 I or 4 H bytes each (fp32 partials) stay below 2^32, so that the offset of a row
+    // past the tile's valid ones never wraps into them
+    if (H > (1 << 20) || I > (1 << 20)) return MOK_ERROR_INVALID_VALUE;
     // the layer's own bounds: 32-bit byte offsets into x / out, h / dh and a weight gradient
     if (T >= (int64_t(1) << 31)) return MOK_ERROR_INVALID_VALUE;
     if (T * (int64_t)H * 2 >= (int64_t(1) << 31)) return MOK_ERROR_INVALID_VALUE;

@@ -112,7 +112,8 @@ def test_norm_backward_refuses_shapes_and_small_workspaces():
 
 BAD_FFN = [dict(T=-1), dict(H=0), dict(I=0), dict(H=96), dict(I=32), dict(precision=mok.MOK_MXFP8, H=192),
            dict(precision=mok.MOK_MXFP8, I=64), dict(precision=mok.MOK_MXFP8_WGRAD), dict(precision=9),
-           dict(T=1 << 17, H=8192), dict(T=1 << 19, I=1024), dict(H=32768, I=32704), dict(H=32704, I=32768)]
+           dict(T=1 << 17, H=8192), dict(T=1 << 19, I=1024), dict(H=32768, I=32704), dict(H=32704, I=32768),
+           dict(T=1, H=64, I=(1 << 20) + 64), dict(T=1, H=(1 << 20) + 64, I=64)]
 
 
 @pytest.mark.parametrize("over", BAD_FFN)
@@ -121,6 +122,12 @@ def test_ffn_refuses_shapes(over):
     s.update(over)
     need = ctypes.c_size_t()
     assert mok.mok_ffn_query_size(mok.mok_ffn_shape(**s), ctypes.byref(need)) == BAD
+
+
+@pytest.mark.parametrize("shape", [(1, 64, 1 << 20, 0), (1, 1 << 20, 64, 0), (1, 128, 1 << 20, 1), ((1 << 24) - 1, 64, 64, 0)])
+def test_ffn_shapes_at_the_bounds_accepted(shape):
+    need = ctypes.c_size_t()
+    assert mok.mok_ffn_query_size(mok.mok_ffn_shape(*shape), ctypes.byref(need)) == mok.MOK_OK and need.value > 0
 
 
 @pytest.mark.parametrize("precision", [mok.MOK_BF16, mok.MOK_MXFP8])
