@@ -257,3 +257,48 @@ def test_repeats_streams_and_graphs_give_the_same_bits(mx, T):
         torch.cuda.synchronize()
         for n, t in ref.items():
             assert torch.equal(got[n], t), (rep, n)
+
+
+@pytest.mark.parametrize("H,I", [(64, 1 << 20), (1 << 20, 64)])
+def test_widest_shapes(H, I):
+    # the widest rows: offsets of rows past the tile's valid ones reach 2^32 and must not wrap into them
+    T = 3
+    print(f"[ffn] widest T={T} H={H} I={I}", flush=True)
+    c = Case(T, H, I, False, 71)
+    o = c.oracle()
+    out, h = c.forward()
+    ref, rh, _ = B.ffn(**o)
+    g = c.backward(h)
+    r = B.ffn_backward(o["x"], o["wg"], o["wu"], o["wd"], host_f64(h), host_f64(c.dy), o["addend"])
+    errs = dict(out=L.rel_frobenius(host_f64(out), ref), h=L.rel_frobenius(host_f64(h), rh))
+    errs.update({n: L.rel_frobenius(host_f64(g[n]), r[n]) for n in g})
+    assert all(v < 1e-2 for v in errs.values()), errs
+
+
+def test_longest_batch():
+    # T * I * 4 one row short of 2 GiB: the largest batch the offsets allow, at the narrowest width
+    T, H, I = (1 << 23) - 1, 64, 64
+    print(f"[ffn] longest T={T}", flush=True)
+    c = Case(T, H, I, False, 81)
+    out, h = c.forward()
+    g = c.backward(h)
+    pick = torch.cat([torch.arange(0, 300), torch.arange(T // 2 - 150, T // 2 + 150), torch.arange(T - 300, T)]).to(DEV)
+    f = lambda t: host_f64(t[pick])  # noqa: E731
+    wg, wu, wd = (host_f64(w) for w in (c.wg, c.wu, c.wd))
+    ref, rh, _ = B.ffn(f(c.x), wg, wu, wd, f(c.add))
+    r = B.ffn_backward(f(c.x), wg, wu, wd, f(h), f(c.dy), f(c.add))
+    for got, want in ((f(out), ref), (f(h), rh), (f(g["dx"]), r["dx"])):
+        assert float(np.max(L.rel_rows(got, want))) < 2e-2
+    # weight gradients over all rows, in fp64 chunk by chunk on the device
+    dw = {n: torch.zeros(g[n].shape, dtype=torch.float64, device=DEV) for n in ("dw_gate", "dw_up", "dw_down")}
+    for a in range(0, T, 1 << 20):
+        x, dy, hh = (t[a:a + (1 << 20)].double() for t in (c.x, c.dy, h))
+        hg, hu = hh[:, :I], hh[:, I:]
+        s = torch.sigmoid(hg)
+        da = dy @ c.wd.double().T
+        dw["dw_gate"] += x.T @ (da * hu * s * (1 + hg * (1 - s)))
+        dw["dw_up"] += x.T @ (da * hg * s)
+        dw["dw_down"] += (hg * s * hu).T @ dy
+    # fp32 sums of 2^23 products: random roundings, about 2^-24 sqrt(2^23) of the sum's size, beside bf16's 2^-8
+    for n, want in dw.items():
+        assert float((g[n].double() - want).norm() / want.norm()) < 1e-2, n
