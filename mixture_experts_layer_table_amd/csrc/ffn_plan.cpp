@@ -34,15 +34,15 @@ size_t part_bytes(int64_t T, int H, int I) {
 // of them) and `steps` K-steps: the least estimated time over the choices,
 // from the rounds of tiles over the compute units, the time of a K-step, and
 // the join with its partials' traffic. The constants were fitted to kernel
-// traces over T from 1 to 4,096 at 7,168 x 2,048, 4,096 x 1,024 and 1,024 x 512
-// (choices 2% slower than the best measured one in the mean, 20% at most).
+// traces of 15 lengths from 3 to 4,096 rows at 7,168 x 2,048, 4,096 x 1,024,
+// 2,048 x 768, 1,024 x 512 and 512 x 2,048: the choices are 1.4% slower than the
+// best measured ones in the mean, 25% at most.
 // Depends on the shape alone, so the bits of a result do too.
 FfnSplit choose(int64_t T, int64_t N, int64_t n_tiles, int steps, bool mx) {
     FfnSplit best{256, 1, steps};
     double least = 1e30;
     for (int bm : {256, 128}) {
-        const double step_us = bm == 256 ? (mx ? 0.9 : 0.85) : (mx ? 0.74 : 0.5);
-        const double tile_us = bm == 256 ? 6.0 : 4.0;
+        const double step_us = bm == 256 ? (mx ? 0.85 : 0.75) : (mx ? 0.74 : 0.5);
         const int64_t tiles = ceil_div(T, bm) * n_tiles;
         for (int s = 1; s <= kMaxSplits; ++s) {
             int len = (int)ceil_div(steps, s);
@@ -50,8 +50,8 @@ FfnSplit choose(int64_t T, int64_t N, int64_t n_tiles, int steps, bool mx) {
             if (s > 1 && len < 2) break;
             if (s > 1 && ceil_div(steps, len) != s) continue;
             if (s > 1 && (size_t)(s * T * N * 4) > kPartBytes) break;
-            double us = (double)ceil_div(tiles * s, kUnits) * (len * step_us + tile_us);
-            if (s > 1) us += 5.5 + 0.1 * s + (double)s * T * N * 8 / 5.0e6;
+            double us = (double)ceil_div(tiles * s, kUnits) * (len * step_us + 5.0);
+            if (s > 1) us += 6.0 + 0.1 * s + (double)s * T * N * 8 / 5.0e6;
             if (us < least) {
                 least = us;
                 best = FfnSplit{bm, s, len};
