@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 
 __version__ = "0.1.0"
@@ -600,9 +601,25 @@ _BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
 # error's wording to _require; pointers go to ctypes as plain integers.
 
 def _need(t, name, dtype, shape, device):
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
-            and t.device == device):
-        _require(t, name, dtype, shape, device)
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device:
+            return
+    except AttributeError:
+        pass
+    _require(t, name, dtype, shape, device)
+
+
+# Argument structs by value (the library only reads them) and sizes by shape.
+_norm_shape = functools.lru_cache(256)(mok_norm_shape)
+_ffn_shape = functools.lru_cache(256)(mok_ffn_shape)
+
+
+@functools.lru_cache(256)
+def _norm_backward_bytes(T, H, sd) -> int:
+    need = ctypes.c_size_t()
+    _check(mok_add_rmsnorm_backward_size(mok_norm_shape(T, H, sd, 0.0, 0.0), ctypes.byref(need)),
+           "mok_add_rmsnorm_backward_size")
+    return need.value
 
 
 def _addr(t):
@@ -724,7 +741,7 @@ def add_rmsnorm(x, weight, eps: float, residual=None, p: float = 0.0, rng=None, 
             r["y_elems"], r["y_scales"] = torch.empty_like(x, dtype=_U8), x.new_empty((T, H // 32), dtype=_U8)
     else:
         r = {n: outs[n] for n in ("sum", "rstd") + (("y",) if y else ()) + (("y_elems", "y_scales") if mxfp8 else ())}
-    _check(_lib.mok_add_rmsnorm(ctypes.byref(mok_norm_shape(T, H, sd, eps, p)), x.data_ptr(), _addr(residual),
+    _check(_lib.mok_add_rmsnorm(ctypes.byref(_norm_shape(T, H, sd, eps, p)), x.data_ptr(), _addr(residual),
                                 weight.data_ptr(), state, r["sum"].data_ptr(), r["y"].data_ptr() if y else None,
                                 r["y_elems"].data_ptr() if mxfp8 else None,
                                 r["y_scales"].data_ptr() if mxfp8 else None, r["rstd"].data_ptr(), _raw_stream(dev.index)),
@@ -759,21 +776,20 @@ def add_rmsnorm_backward(dy, sum, weight, rstd, dsum=None, p: float = 0.0, rng=N
     if _elsewhere(dev):
         with torch.cuda.device(dev):
             return add_rmsnorm_backward(dy, sum, weight, rstd, dsum, p, rng, grads, workspace)
-    s = mok_norm_shape(T, H, sd, 0.0, p)
-    need = ctypes.c_size_t()
-    _check(_lib.mok_add_rmsnorm_backward_size(ctypes.byref(s), ctypes.byref(need)), "mok_add_rmsnorm_backward_size")
+    need = _norm_backward_bytes(T, H, sd)
     if workspace is None:
-        workspace = sum.new_empty((need.value,), dtype=_U8)
+        workspace = sum.new_empty((need,), dtype=_U8)
     else:
-        _require_bytes(workspace, "workspace", need.value, dev)
+        _require_bytes(workspace, "workspace", need, dev)
+        need = workspace.numel()
     if grads is None:
-        g = dict(dresidual=torch.empty_like(sum), dweight=sum.new_empty((H,), dtype=_F32))
+        g = dict(dresidual=torch.empty_like(sum), dweight=torch.empty_like(weight, dtype=_F32))
         if separate:
             g["dx"] = torch.empty_like(dy)
     else:
         g = {n: grads[n] for n in ("dresidual", "dweight") + (("dx",) if separate else ())}
-    _check(_lib.mok_add_rmsnorm_backward(ctypes.byref(s), workspace.data_ptr(), workspace.numel(), dy.data_ptr(),
-                                         sum.data_ptr(), weight.data_ptr(), rstd.data_ptr(), _addr(dsum), state,
+    _check(_lib.mok_add_rmsnorm_backward(ctypes.byref(_norm_shape(T, H, sd, 0.0, p)), workspace.data_ptr(), need,
+                                         dy.data_ptr(), sum.data_ptr(), weight.data_ptr(), rstd.data_ptr(), _addr(dsum), state,
                                          g["dresidual"].data_ptr(), g["dx"].data_ptr() if separate else None,
                                          g["dweight"].data_ptr(), _raw_stream(dev.index)), "mok_add_rmsnorm_backward")
     if not separate:
@@ -871,7 +887,7 @@ def ffn_forward(ws: FfnWorkspace, x, weights: mok_weights, addend=None, out=None
         out = buf.new_empty((T, H), dtype=_BF16)
     if h is None and save_h:
         h = buf.new_empty((T, 2 * I), dtype=_BF16)
-    _check(_lib.mok_ffn_forward(ctypes.byref(mok_ffn_shape(T, H, I, ws.precision)), buf.data_ptr(), buf.numel(), rows,
+    _check(_lib.mok_ffn_forward(ctypes.byref(_ffn_shape(T, H, I, ws.precision)), buf.data_ptr(), buf.numel(), rows,
                                 elems, scales, ctypes.byref(weights), _addr(addend), out.data_ptr(), _addr(h),
                                 _raw_stream(dev.index)), "mok_ffn_forward")
     return out, h
@@ -899,7 +915,7 @@ def ffn_backward(ws: FfnWorkspace, x, weights: mok_weights, h, dy, addend=None, 
         with torch.cuda.device(dev):
             return ffn_backward(ws, x, weights, h, dy, addend, grads)
     g = {n: buf.new_empty(sh, dtype=_BF16) if grads is None else grads[n] for n, sh in shapes.items()}
-    _check(_lib.mok_ffn_backward(ctypes.byref(mok_ffn_shape(T, H, I, ws.precision)), buf.data_ptr(), buf.numel(),
+    _check(_lib.mok_ffn_backward(ctypes.byref(_ffn_shape(T, H, I, ws.precision)), buf.data_ptr(), buf.numel(),
                                  x.data_ptr(), ctypes.byref(weights), h.data_ptr(), dy.data_ptr(), _addr(addend),
                                  g["dx"].data_ptr(), g["dw_gate"].data_ptr(), g["dw_up"].data_ptr(),
                                  g["dw_down"].data_ptr(), _raw_stream(dev.index)), "mok_ffn_backward")

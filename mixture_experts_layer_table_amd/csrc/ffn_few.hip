@@ -9,10 +9,13 @@
 //   1. gate/up, the contraction axis cut into few enough runs that the second
 //      kernel can add them itself (BF16), or not cut at all (MXFP8, whose
 //      weights are contiguous along it);
-//   2. down: every workgroup first makes a = silu(h_g) h_u for itself, after its
-//      weight loads are on their way, then finishes whole outputs.
+//   2. down: every workgroup makes a = silu(h_g) h_u for itself, asked for ahead
+//      of its weights, then finishes whole outputs.
 // a stays in fp32 in BF16 mode (one rounding fewer than the tile kernels).
 // Sums run in a fixed order: lane, wave, run.
+//
+// Measured, one row of 7,168 x 2,048: BF16 23 us (gate/up 13, down 10), MXFP8 15
+// (9 and 6). Each kernel's launch, first loads and lane sums are 4 to 5 us.
 //
 // Which calls come here is plan_few's rule (ffn_plan.cpp). The cost that grows
 // with the rows is each lane's sums, not the weights: at 7,168 x 2,048 two BF16
