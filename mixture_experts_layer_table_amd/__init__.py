@@ -675,8 +675,8 @@ def dropout(x, rng, p: float, residual=None, out=None):
             return dropout(x, rng, p, residual, out)
     if out is None:
         out = torch.empty_like(like)
-    _check(_lib.mok_dropout(x.data_ptr(), _addr(residual), x.numel(), p, state, sd, out.data_ptr(), _raw_stream(dev.index)),
-           "mok_dropout")
+    _check(_lib.mok_dropout(x.data_ptr(), _addr(residual), x.numel(), p, state, sd, out.data_ptr(),
+                            _raw_stream(dev.index)), "mok_dropout")
     return out
 
 
@@ -744,8 +744,8 @@ def add_rmsnorm(x, weight, eps: float, residual=None, p: float = 0.0, rng=None, 
     _check(_lib.mok_add_rmsnorm(ctypes.byref(_norm_shape(T, H, sd, eps, p)), x.data_ptr(), _addr(residual),
                                 weight.data_ptr(), state, r["sum"].data_ptr(), r["y"].data_ptr() if y else None,
                                 r["y_elems"].data_ptr() if mxfp8 else None,
-                                r["y_scales"].data_ptr() if mxfp8 else None, r["rstd"].data_ptr(), _raw_stream(dev.index)),
-           "mok_add_rmsnorm")
+                                r["y_scales"].data_ptr() if mxfp8 else None, r["rstd"].data_ptr(),
+                                _raw_stream(dev.index)), "mok_add_rmsnorm")
     return r
 
 
@@ -789,9 +789,10 @@ def add_rmsnorm_backward(dy, sum, weight, rstd, dsum=None, p: float = 0.0, rng=N
     else:
         g = {n: grads[n] for n in ("dresidual", "dweight") + (("dx",) if separate else ())}
     _check(_lib.mok_add_rmsnorm_backward(ctypes.byref(_norm_shape(T, H, sd, 0.0, p)), workspace.data_ptr(), need,
-                                         dy.data_ptr(), sum.data_ptr(), weight.data_ptr(), rstd.data_ptr(), _addr(dsum), state,
-                                         g["dresidual"].data_ptr(), g["dx"].data_ptr() if separate else None,
-                                         g["dweight"].data_ptr(), _raw_stream(dev.index)), "mok_add_rmsnorm_backward")
+                                         dy.data_ptr(), sum.data_ptr(), weight.data_ptr(), rstd.data_ptr(),
+                                         _addr(dsum), state, g["dresidual"].data_ptr(),
+                                         g["dx"].data_ptr() if separate else None, g["dweight"].data_ptr(),
+                                         _raw_stream(dev.index)), "mok_add_rmsnorm_backward")
     if not separate:
         g["dx"] = g["dresidual"]
     return g

@@ -15,6 +15,8 @@ bool aligned4(const void *p) { return p != nullptr && (reinterpret_cast<uintptr_
 bool dev_ok(const void *p) { return p != nullptr && aligned16(p); }
 bool dev_ok_or_null(const void *p) { return aligned16(p); }
 
+constexpr int64_t kMaxDropout = int64_t(1) << 40;   // elements of one dropout call
+
 bool stream_ok(int32_t dtype) { return dtype == MOK_STREAM_BF16 || dtype == MOK_STREAM_F32; }
 // p in [0, 1); the state is read only where something can be dropped
 bool drop_ok(float p, const uint64_t *rng) {
@@ -222,7 +224,7 @@ mok_status mok_route_backward(const int32_t *topk_ids, const float *topk_w, cons
 
 mok_status mok_dropout(const void *x, const void *residual, int64_t n, float p, const uint64_t *rng,
                        int32_t stream_dtype, void *out, void *stream) {
-    if (n < 0 || n >= (int64_t(1) << 40) || !stream_ok(stream_dtype) || !drop_ok(p, rng)) return MOK_ERROR_INVALID_VALUE;
+    if (n < 0 || n >= kMaxDropout || !stream_ok(stream_dtype) || !drop_ok(p, rng)) return MOK_ERROR_INVALID_VALUE;
     if (n == 0) return MOK_OK;
     if (!dev_ok(x) || !dev_ok_or_null(residual) || !dev_ok(out)) return MOK_ERROR_INVALID_VALUE;
     const bool f32 = stream_dtype == MOK_STREAM_F32;
@@ -236,7 +238,7 @@ mok_status mok_dropout(const void *x, const void *residual, int64_t n, float p, 
 
 mok_status mok_dropout_backward(const void *dy, int64_t n, float p, const uint64_t *rng, int32_t stream_dtype,
                                 void *dx, void *stream) {
-    if (n < 0 || n >= (int64_t(1) << 40) || !stream_ok(stream_dtype) || !drop_ok(p, rng)) return MOK_ERROR_INVALID_VALUE;
+    if (n < 0 || n >= kMaxDropout || !stream_ok(stream_dtype) || !drop_ok(p, rng)) return MOK_ERROR_INVALID_VALUE;
     if (n == 0) return MOK_OK;
     if (!dev_ok(dy) || !dev_ok(dx)) return MOK_ERROR_INVALID_VALUE;
     const bool f32 = stream_dtype == MOK_STREAM_F32;
@@ -382,9 +384,11 @@ mok_status mok_ffn_forward(const mok_ffn_shape *shape, void *workspace, size_t w
     const size_t n = (size_t)p.T * p.H;
     const Span so{out, n * 2}, sh{h, (size_t)p.T * p.I * 4}, sws{workspace, p.total}, sadd{addend, n * 2};
     const Span outs[] = {so, sh, sws};
-    const Span ins[] = {{p.mx ? nullptr : x, n * 2}, {p.mx ? x_elems : nullptr, n}, {p.mx ? x_scales : nullptr, n / 32}};
+    const Span ins[] = {
+        {p.mx ? nullptr : x, n * 2}, {p.mx ? x_elems : nullptr, n}, {p.mx ? x_scales : nullptr, n / 32}};
     const FfnWeightSpans ws = ffn_weight_spans(p, w);
-    if (!apart(outs) || overlap_partly(so, sadd) || overlap(sh, sadd) || overlap(sws, sadd)) return MOK_ERROR_INVALID_VALUE;
+    if (!apart(outs) || overlap_partly(so, sadd) || overlap(sh, sadd) || overlap(sws, sadd))
+        return MOK_ERROR_INVALID_VALUE;
     for (const Span &o : outs)
         if (any_overlap(o, ins) || any_overlap(o, ws.s)) return MOK_ERROR_INVALID_VALUE;
     (void)hipGetLastError();
@@ -411,7 +415,8 @@ mok_status mok_ffn_backward(const mok_ffn_shape *shape, void *workspace, size_t 
     const FfnWeightSpans ws = ffn_weight_spans(p, w);
     if (!apart(outs) || overlap_partly(sdx, sadd)) return MOK_ERROR_INVALID_VALUE;
     for (const Span &o : outs)
-        if (any_overlap(o, ins) || any_overlap(o, ws.s) || (o.p != dx && overlap(o, sadd))) return MOK_ERROR_INVALID_VALUE;
+        if (any_overlap(o, ins) || any_overlap(o, ws.s) || (o.p != dx && overlap(o, sadd)))
+            return MOK_ERROR_INVALID_VALUE;
     (void)hipGetLastError();
     return launch_ffn_backward(p, workspace, static_cast<const uint16_t *>(x), *w, static_cast<const uint16_t *>(h),
                                static_cast<const uint16_t *>(dy), static_cast<const uint16_t *>(addend),

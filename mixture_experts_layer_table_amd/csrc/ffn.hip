@@ -32,7 +32,8 @@ using CfgS = TileCfg<128, 256, 2, 4, 6>;   // 6 stages of 24 KiB
 // CfgS at half the LDS and at most 128 registers: two workgroups per compute
 // unit, one's stores beside the other's loads
 using CfgW = TileCfg<128, 256, 2, 4, 3, 4>;
-static_assert(CfgA::BN == kTileN && CfgS::BN == kTileN && CfgW::BN == kTileN, "host sizing assumes kTileN-column tiles");
+static_assert(CfgA::BN == kTileN && CfgS::BN == kTileN && CfgW::BN == kTileN,
+              "host sizing assumes kTileN-column tiles");
 
 struct FfnArgs {
     int T, H, I, n_tiles, splits, len;
@@ -106,13 +107,14 @@ struct FfnGateUp {
                         v[j] = hg * sigmoidf_(hg) * hu;
                     }
                     FS::put(area + FS::frag_off(fn, g4, lane),
-                            make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])));
+                            pack4(v[0], v[1], v[2], v[3]));
                 }
             // the first half of each staged row: 32 values of i; the other lanes store nothing
 #pragma unroll
             for (int p = 0; p < FS::PASSES; ++p) {
                 const int m = wm * C::WM + fm * 32 + FS::pass_row(p, lane), cc = FS::pass_col(lane);
-                bstore8_nt(adst, m < t.rows && cc < C::WN / 2 ? a0 + (uint32_t)m * 64u + 2u * (uint32_t)cc : kOutOfRange, 0,
+                const bool ok = m < t.rows && cc < C::WN / 2;
+                bstore8_nt(adst, ok ? a0 + (uint32_t)m * 64u + 2u * (uint32_t)cc : kOutOfRange, 0,
                            FS::get(area + FS::pass_off(p, lane)));
             }
         }
@@ -236,10 +238,11 @@ struct FfnDA {
                     const uint2 hg2 = FS::get(sg + o), hu2 = FS::get(su + o);
                     GluGrad r[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) r[j] = glu_backward(acc[fm][fn][g4 * 4 + j], bf16_at(hg2, j), bf16_at(hu2, j));
-                    FS::put(sg + o, make_uint2(pack_bf16x2(r[0].dg, r[1].dg), pack_bf16x2(r[2].dg, r[3].dg)));
-                    FS::put(su + o, make_uint2(pack_bf16x2(r[0].du, r[1].du), pack_bf16x2(r[2].du, r[3].du)));
-                    FS::put(sa + o, make_uint2(pack_bf16x2(r[0].a, r[1].a), pack_bf16x2(r[2].a, r[3].a)));
+                    for (int j = 0; j < 4; ++j)
+                        r[j] = glu_backward(acc[fm][fn][g4 * 4 + j], bf16_at(hg2, j), bf16_at(hu2, j));
+                    FS::put(sg + o, pack4(r[0].dg, r[1].dg, r[2].dg, r[3].dg));
+                    FS::put(su + o, pack4(r[0].du, r[1].du, r[2].du, r[3].du));
+                    FS::put(sa + o, pack4(r[0].a, r[1].a, r[2].a, r[3].a));
                 }
             __builtin_amdgcn_sched_barrier(0);
             if (fm + 1 < C::FM) load_h(fm + 1);   // in flight while this fragment's rows are stored
@@ -403,8 +406,8 @@ hipError_t backward_bf16(const FfnPlan &p, char *ws, const uint16_t *x, const mo
         if (e != hipSuccess) return e;
         if (p.da.splits > 1) {
             KernelTimer tm("ffn_join_da", st);
-            ffn_join_da<false><<<join_grid(p.T, p.I), 256, 0, st>>>(a.part, p.da.splits, a.T, a.I, h, a.dh, a.a, nullptr,
-                                                                    nullptr);
+            ffn_join_da<false><<<join_grid(p.T, p.I), 256, 0, st>>>(a.part, p.da.splits, a.T, a.I, h, a.dh, a.a,
+                                                                    nullptr, nullptr);
         }
     }
     a.x = a.dh;

@@ -179,9 +179,9 @@ __device__ __forceinline__ f32x4_t act_of(const FewArgs &a, int rows, int e, con
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = g[j] * sigmoidf_(g[j]) * u[j];
     if (a.h && save) {
-        *reinterpret_cast<uint2 *>(a.h + (int64_t)t * 2 * a.I + i) = make_uint2(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]));
+        *reinterpret_cast<uint2 *>(a.h + (int64_t)t * 2 * a.I + i) = pack4(g[0], g[1], g[2], g[3]);
         *reinterpret_cast<uint2 *>(a.h + (int64_t)t * 2 * a.I + a.I + i) =
-            make_uint2(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]));
+            pack4(u[0], u[1], u[2], u[3]);
     }
     return v;
 }
@@ -206,17 +206,16 @@ __global__ __launch_bounds__(kThreads, 2) void few_down(FewArgs a, int rows) {
         for (int j = 0; j < 8; ++j) acc[t][j] = 0.0f;
     // The first 4 values of i of each thread are asked for ahead of the weights
     // (loads return in order), so that a is ready when the weights arrive.
-    const bool mine = (int)threadIdx.x * 4 < T * I;
+    const int e0 = (int)threadIdx.x * 4;
     f32x4_t hg[kJoinBatch], hu[kJoinBatch];
-    if (mine) load_runs(a, rows, (int)threadIdx.x * 4, hg, hu);
+    if (e0 < T * I) load_runs(a, rows, e0, hg, hu);
     for (int b = 0; b < n; b += kBatch) {
         uint4 wv[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) wv[i] = load16(w, v0, (uint32_t)(b + i) * step);   // rows past I: zeros
         if (b == 0) {
-            if (mine) *reinterpret_cast<f32x4_t *>(as + threadIdx.x * 4) = act_of(a, rows, (int)threadIdx.x * 4, hg, hu, strip == 0);
-            for (int e = (int)(threadIdx.x + kThreads) * 4; e < T * I; e += kThreads * 4) {
-                load_runs(a, rows, e, hg, hu);
+            for (int e = e0; e < T * I; e += kThreads * 4) {
+                if (e != e0) load_runs(a, rows, e, hg, hu);
                 *reinterpret_cast<f32x4_t *>(as + e) = act_of(a, rows, e, hg, hu, strip == 0);
             }
             __syncthreads();
@@ -260,16 +259,19 @@ __global__ __launch_bounds__(kThreads, 2) void few_down(FewArgs a, int rows) {
 // 2^(e - 127) for a scale byte e (0 is the subnormal 2^-127).
 __device__ __forceinline__ float scale_value(uint32_t e) { return __uint_as_float(e ? e << 23 : 0x00400000u); }
 
+// The values of 4 E4M3 codes.
+__device__ __forceinline__ f32x4_t unpack_fp8x4(uint32_t w) {
+    const f32x2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
+    const f32x2_t hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+    return f32x4_t{lo.x, lo.y, hi.x, hi.y};
+}
 __device__ __forceinline__ void unpack_fp8x16(const uint4 &v, float (&f)[16]) {
-    typedef float v2f __attribute__((ext_vector_type(2)));
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], true);
-        f[4 * i] = lo.x;
-        f[4 * i + 1] = lo.y;
-        f[4 * i + 2] = hi.x;
-        f[4 * i + 3] = hi.y;
+        const f32x4_t u = unpack_fp8x4(w[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[4 * i + j] = u[j];
     }
 }
 
@@ -325,20 +327,20 @@ __global__ __launch_bounds__(kThreads, 2) void few_gate_up8(Few8Args a, int rows
             float gf[16], uf[16];
             unpack_fp8x16(gv[c], gf);
             unpack_fp8x16(uv[c], uf);
-            const float gq = scale_value(ge[c]), uq = scale_value(ue[c]);
 #pragma unroll
             for (int t = 0; t < T; ++t) {
                 float xf[16];
                 unpack_fp8x16(xv[t][c], xf);
-                const float xq = scale_value(xe[t][c]);
                 float dg = 0.0f, du = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     dg = __builtin_fmaf(gf[j], xf[j], dg);
                     du = __builtin_fmaf(uf[j], xf[j], du);
                 }
-                sg[t] += dg * gq * xq;   // half of one 32-block: powers of two, exact short of under- and overflow
-                su[t] += du * uq * xq;
+                // half of one 32-block; the two scales as one exponent, so that neither
+                // alone can over- or underflow a sum whose value is in range
+                sg[t] += __builtin_ldexpf(dg, (int)(ge[c] + xe[t][c]) - 254);
+                su[t] += __builtin_ldexpf(du, (int)(ue[c] + xe[t][c]) - 254);
             }
         }
     }
@@ -394,10 +396,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_down8(Few8Args a, int rows) {
                 const float v[4] = {p[0], p[1], p[2], p[3]};
                 uint32_t sc;
                 const uint32_t code = quantize_lane4(v, sc);
-                typedef float v2f __attribute__((ext_vector_type(2)));
-                const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)code, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)code, true);
-                const float q = scale_value(sc);
-                *reinterpret_cast<f32x4_t *>(few_lds + e) = f32x4_t{lo.x * q, lo.y * q, hi.x * q, hi.y * q};
+                *reinterpret_cast<f32x4_t *>(few_lds + e) = unpack_fp8x4(code) * scale_value(sc);
             }
             __syncthreads();
         }
@@ -459,8 +458,8 @@ hipError_t ffn_few_forward(const FfnPlan &p, char *ws, const uint16_t *x, const 
         constexpr int T = decltype(tc)::value;
         {
             KernelTimer tm("ffn_few_gate_up", st);
-            few_gate_up<T><<<(unsigned)(p.I / 64 * p.few_runs), kThreads, sizeof(float) * T * (p.few_run_rows + kWaves * 128),
-                             st>>>(a, rows);
+            const size_t lds = sizeof(float) * T * (p.few_run_rows + kWaves * 128);
+            few_gate_up<T><<<(unsigned)(p.I / 64 * p.few_runs), kThreads, lds, st>>>(a, rows);
         }
         KernelTimer tm("ffn_few_down", st);
         const unsigned grid = (unsigned)(ceil_div(p.H / 32, 2 * kXcds) * 2 * kXcds);
@@ -470,7 +469,8 @@ hipError_t ffn_few_forward(const FfnPlan &p, char *ws, const uint16_t *x, const 
 }
 
 hipError_t ffn_few_mx_forward(const FfnPlan &p, char *ws, const uint8_t *x_elems, const uint8_t *x_scales,
-                              const mok_weights &w, const uint16_t *addend, uint16_t *out, uint16_t *h, hipStream_t st) {
+                              const mok_weights &w, const uint16_t *addend, uint16_t *out, uint16_t *h,
+                              hipStream_t st) {
     Few8Args a{p.H, p.I, lanes_for(p.H), x_elems, x_scales, w.gate_elems, w.gate_scales, w.up_elems, w.up_scales,
                w.down_elems, w.down_scales, addend, out, h, reinterpret_cast<float *>(ws + p.part)};
     const int rows = (int)p.T;
@@ -482,8 +482,8 @@ hipError_t ffn_few_mx_forward(const FfnPlan &p, char *ws, const uint8_t *x_elems
         }
         a.lanes = lanes_for(p.I);
         KernelTimer tm("ffn_few_down_mx", st);
-        few_down8<T><<<(unsigned)ceil_div(p.H, kWaves * (64 / a.lanes) * kRowsPerGroup), kThreads, sizeof(float) * T * p.I,
-                       st>>>(a, rows);
+        const unsigned grid = (unsigned)ceil_div(p.H, kWaves * (64 / a.lanes) * kRowsPerGroup);
+        few_down8<T><<<grid, kThreads, sizeof(float) * T * p.I, st>>>(a, rows);
     });
     return hipGetLastError();
 }

@@ -290,9 +290,9 @@ struct FfnDA8 : Ffn8Base<Cfg> {
                         dg.v[e + j] = g.dg;
                         du.v[e + j] = g.du;
                     }
-                    FS::put(sg + o, make_uint2(pack_bf16x2(dg.v[e], dg.v[e + 1]), pack_bf16x2(dg.v[e + 2], dg.v[e + 3])));
-                    FS::put(su + o, make_uint2(pack_bf16x2(du.v[e], du.v[e + 1]), pack_bf16x2(du.v[e + 2], du.v[e + 3])));
-                    FS::put(sa + o, make_uint2(pack_bf16x2(av[0], av[1]), pack_bf16x2(av[2], av[3])));
+                    FS::put(sg + o, pack4(dg.v[e], dg.v[e + 1], dg.v[e + 2], dg.v[e + 3]));
+                    FS::put(su + o, pack4(du.v[e], du.v[e + 1], du.v[e + 2], du.v[e + 3]));
+                    FS::put(sa + o, pack4(av[0], av[1], av[2], av[3]));
                 }
                 const Enc16 qg = encode_block16(dg), qu = encode_block16(du);
 #pragma unroll
@@ -381,7 +381,8 @@ __global__ __launch_bounds__(P::C::NT, 2) void ffn_gemm8(Ffn8Args args) {
 
 // dW_gate | dW_up and dW_down (BF16 tiles), then dx (block-scaled tiles), in one launch.
 template <class PX, class PW>
-__global__ __launch_bounds__(PX::C::NT, 2) void ffn_grads8(FfnWgradArgs gu, FfnWgradArgs wd, Ffn8Args ax, int g0, int g1) {
+__global__ __launch_bounds__(PX::C::NT, 2) void ffn_grads8(FfnWgradArgs gu, FfnWgradArgs wd, Ffn8Args ax, int g0,
+                                                           int g1) {
     extern __shared__ __attribute__((aligned(1024))) char lds_raw[];
     const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds_raw;
     int b = (int)blockIdx.x;
@@ -452,7 +453,8 @@ hipError_t ffn_mx_forward(const FfnPlan &p, char *ws, const uint8_t *x_elems, co
     if (e != hipSuccess) return e;
     if (p.gate_up.splits > 1) {
         KernelTimer tm("ffn_join_act", st);
-        ffn_join_act<true><<<join_grid(p.T, p.I), 256, 0, st>>>(a.part, p.gate_up.splits, a.T, a.I, h, nullptr, a.q, a.qs);
+        ffn_join_act<true><<<join_grid(p.T, p.I), 256, 0, st>>>(a.part, p.gate_up.splits, a.T, a.I, h, nullptr, a.q,
+                                                                a.qs);
     }
     a.x = a.q;
     a.xs = a.qs;
@@ -498,7 +500,8 @@ hipError_t ffn_mx_backward(const FfnPlan &p, char *ws, const uint16_t *x, const 
         if (e != hipSuccess) return e;
         if (p.da.splits > 1) {
             KernelTimer tm("ffn_join_da", st);
-            ffn_join_da<true><<<join_grid(p.T, p.I), 256, 0, st>>>(a.part, p.da.splits, a.T, a.I, h, a.dh, a.a, a.q, a.qs);
+            ffn_join_da<true><<<join_grid(p.T, p.I), 256, 0, st>>>(a.part, p.da.splits, a.T, a.I, h, a.dh, a.a, a.q,
+                                                                   a.qs);
         }
     }
     a.x = a.q;
@@ -514,10 +517,11 @@ hipError_t ffn_mx_backward(const FfnPlan &p, char *ws, const uint16_t *x, const 
     a.len = p.dx.len;
     const FfnWgradArgs gu{a.T, p.H, 2 * p.I, p.I, p.I, x, a.dh, dw_gate, dw_up};
     const FfnWgradArgs wd{a.T, p.I, p.H, p.H, p.H, a.a, dy, dw_down, nullptr};
+    const bool small_w = p.wgrad_bm == CfgS::BM;
     if (p.dx.bm == CfgH::BM)
-        e = p.wgrad_bm == CfgS::BM ? launch_grads8<CfgH, CfgS>(gu, wd, a, st) : launch_grads8<CfgH, CfgA>(gu, wd, a, st);
+        e = small_w ? launch_grads8<CfgH, CfgS>(gu, wd, a, st) : launch_grads8<CfgH, CfgA>(gu, wd, a, st);
     else
-        e = p.wgrad_bm == CfgS::BM ? launch_grads8<CfgA, CfgS>(gu, wd, a, st) : launch_grads8<CfgA, CfgA>(gu, wd, a, st);
+        e = small_w ? launch_grads8<CfgA, CfgS>(gu, wd, a, st) : launch_grads8<CfgA, CfgA>(gu, wd, a, st);
     if (e == hipSuccess && p.T > 0 && p.dx.splits > 1) {
         KernelTimer tm("ffn_join_out", st);
         ffn_join_out<<<join_grid(p.T, p.H), 256, 0, st>>>(a.part, p.dx.splits, a.T, a.H, addend, dx);

@@ -46,6 +46,10 @@ inline unsigned ffn_grid(int64_t T, int bm, int64_t n_tiles, int splits) {
 
 // ----------------------------------------------------------------------------- epilogues
 
+__device__ __forceinline__ uint2 pack4(float a, float b, float c, float d) {
+    return make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
+}
+
 __device__ __forceinline__ void bstore16(brsrc_t r, uint32_t voff, float a, float b, float c, float d) {
     typedef uint32_t v4u __attribute__((ext_vector_type(4)));
     const v4u w = {__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d)};
@@ -106,7 +110,7 @@ __device__ __forceinline__ void store_rows_add(const f32x16_t (&acc)[C::FM][C::F
                 float y[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) y[j] = acc[fm][fn][g4 * 4 + j] + bf16_at(b, j);
-                FS::put(o, make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])));
+                FS::put(o, pack4(y[0], y[1], y[2], y[3]));
             }
         __builtin_amdgcn_sched_barrier(0);
         if (fm + 1 < C::FM) load(fm + 1);   // ahead of this fragment's stores: other rows, so also in place
@@ -136,7 +140,9 @@ __device__ __forceinline__ void dense_epilogue(const f32x16_t (&acc)[C::FM][C::F
         store_rows_add<C, LDS_END>(acc, wm, dst, rows_rsrc(addend + o, bytes), row_bytes);
     else
         staged_rows<C, LDS_END>([&](int fm, int fn, int g4, int j) { return acc[fm][fn][g4 * 4 + j]; }, dst,
-                                [&](int fm, int r) -> uint32_t { return (uint32_t)(wm * C::WM + fm * 32 + r) * row_bytes; });
+                                [&](int fm, int r) -> uint32_t {
+                                    return (uint32_t)(wm * C::WM + fm * 32 + r) * row_bytes;
+                                });
 }
 
 // ----------------------------------------------------------------------------- weight gradients
@@ -247,8 +253,8 @@ __global__ __launch_bounds__(256) void ffn_join_act(const float *__restrict__ pa
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = g[j] * sigmoidf_(g[j]) * u[j];
     if (h) {
-        *reinterpret_cast<uint2 *>(h + t * 2 * I + i) = make_uint2(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]));
-        *reinterpret_cast<uint2 *>(h + t * 2 * I + I + i) = make_uint2(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]));
+        *reinterpret_cast<uint2 *>(h + t * 2 * I + i) = pack4(g[0], g[1], g[2], g[3]);
+        *reinterpret_cast<uint2 *>(h + t * 2 * I + I + i) = pack4(u[0], u[1], u[2], u[3]);
     }
     if constexpr (MX) {
         uint32_t sc;
@@ -257,7 +263,7 @@ __global__ __launch_bounds__(256) void ffn_join_act(const float *__restrict__ pa
         if (i % 32 == 0) aqs[(t * I + i) / 32] = (uint8_t)sc;
     } else {
         *reinterpret_cast<uint2 *>(a + ((int64_t)(i / 32) * T + t) * 32 + i % 32) =
-            make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+            pack4(v[0], v[1], v[2], v[3]);
     }
 }
 
@@ -270,7 +276,7 @@ __global__ __launch_bounds__(256) void ffn_join_out(const float *__restrict__ pa
     if (addend) b = reinterpret_cast<const uint2 *>(addend)[idx];
     const f32x4_t s = sum_runs(part + idx * 4, (int64_t)T * N, splits);
     reinterpret_cast<uint2 *>(out)[idx] =
-        make_uint2(pack_bf16x2(s[0] + bf16_at(b, 0), s[1] + bf16_at(b, 1)), pack_bf16x2(s[2] + bf16_at(b, 2), s[3] + bf16_at(b, 3)));
+        pack4(s[0] + bf16_at(b, 0), s[1] + bf16_at(b, 1), s[2] + bf16_at(b, 2), s[3] + bf16_at(b, 3));
 }
 
 // SwiGLU backward of one value: da arrives, h_g and h_u are the saved rows.
@@ -293,7 +299,8 @@ __global__ __launch_bounds__(256) void ffn_join_da(const float *__restrict__ par
     const int64_t t = idx / per;
     const int i = (int)(idx % per) * 4;
     const int64_t row = t * 2 * I;
-    const uint2 hg = *reinterpret_cast<const uint2 *>(h + row + i), hu = *reinterpret_cast<const uint2 *>(h + row + I + i);
+    const uint2 hg = *reinterpret_cast<const uint2 *>(h + row + i);
+    const uint2 hu = *reinterpret_cast<const uint2 *>(h + row + I + i);
     const f32x4_t s = sum_runs(part + t * I + i, (int64_t)T * I, splits);
     float va[4], vg[4], vu[4];
 #pragma unroll
@@ -304,7 +311,7 @@ __global__ __launch_bounds__(256) void ffn_join_da(const float *__restrict__ par
         vu[j] = r.du;
     }
     auto put = [](uint16_t *p, const float (&v)[4]) {
-        *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        *reinterpret_cast<uint2 *>(p) = pack4(v[0], v[1], v[2], v[3]);
     };
     put(a + t * I + i, va);
     put(dh + row + i, vg);
@@ -333,7 +340,8 @@ hipError_t allow_lds(K *kernel, size_t bytes, std::atomic<uint64_t> &done) {
     if (e != hipSuccess) return e;
     const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
     if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
-    const hipError_t r = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    const hipError_t r =
+        hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (r == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
     return r;
 }

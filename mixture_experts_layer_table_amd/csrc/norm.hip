@@ -128,10 +128,12 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_forward(NormFwdArgs a) {
             amax = max(amax, (uint32_t)__shfl_xor((int)amax, 2));
             const uint32_t sb = mx_scale_byte_f32(amax);
             const float q = mx_pow2_neg((int)sb - 127);
-            const uint32_t lo = e4m3x2_scaled(v[i][0] * q, v[i][1] * q) | (e4m3x2_scaled(v[i][2] * q, v[i][3] * q) << 16);
-            const uint32_t hi = e4m3x2_scaled(v[i][4] * q, v[i][5] * q) | (e4m3x2_scaled(v[i][6] * q, v[i][7] * q) << 16);
+            auto codes = [&](int j) {
+                return e4m3x2_scaled(v[i][j] * q, v[i][j + 1] * q) |
+                       (e4m3x2_scaled(v[i][j + 2] * q, v[i][j + 3] * q) << 16);
+            };
             if (ok) {
-                reinterpret_cast<uint2 *>(a.elems)[base + c] = make_uint2(lo, hi);
+                reinterpret_cast<uint2 *>(a.elems)[base + c] = make_uint2(codes(0), codes(4));
                 if ((c & 3) == 0) a.scales[(base + c) >> 2] = (uint8_t)sb;
             }
         }
@@ -281,7 +283,7 @@ RowShape row_shape(int H, int64_t rows) {
 // number of rows. More shares cost their traffic (16,384 x 7,168: 181 us with
 // 384 workgroups, 192 with 1,024), fewer leave units idle (16,384 x 512: 55 us
 // with 256, 23 with 1,024).
-constexpr int kBwdWaves = 3072;
+constexpr int kBwdWaves = 3000;
 int backward_target(int H, int64_t T) { return std::max(1, kBwdWaves / row_shape(H, T).waves); }
 
 template <class F>

@@ -97,7 +97,8 @@ __device__ __forceinline__ void unpack8(const Raw8<E> &r, float (&f)[8]) {
     }
 }
 __device__ __forceinline__ uint4 pack8_bf16(const float (&f)[8]) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
 }
 template <Elem E>
 __device__ __forceinline__ void store8(void *base, int64_t c, const float (&f)[8]) {

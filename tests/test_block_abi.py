@@ -124,7 +124,8 @@ def test_ffn_refuses_shapes(over):
     assert mok.mok_ffn_query_size(mok.mok_ffn_shape(**s), ctypes.byref(need)) == BAD
 
 
-@pytest.mark.parametrize("shape", [(1, 64, 1 << 20, 0), (1, 1 << 20, 64, 0), (1, 128, 1 << 20, 1), ((1 << 23) - 1, 64, 64, 0)])
+@pytest.mark.parametrize("shape", [
+    (1, 64, 1 << 20, 0), (1, 1 << 20, 64, 0), (1, 128, 1 << 20, 1), ((1 << 23) - 1, 64, 64, 0)])
 def test_ffn_shapes_at_the_bounds_accepted(shape):
     need = ctypes.c_size_t()
     assert mok.mok_ffn_query_size(mok.mok_ffn_shape(*shape), ctypes.byref(need)) == mok.MOK_OK and need.value > 0

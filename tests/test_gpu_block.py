@@ -26,8 +26,10 @@ class Block:
         self.gamma = (1.0 + 0.2 * randn((H,), s + 3).float()).to(torch.bfloat16)
         self.logits = randn((T, E), s + 4, torch.float32)
         sc = H ** -0.5
-        self.we = [randn((E, H, I), s + 5, scale=sc), randn((E, H, I), s + 6, scale=sc), randn((E, I, H), s + 7, scale=I ** -0.5)]
-        self.wsh = [randn((H, I), s + 8, scale=sc), randn((H, I), s + 9, scale=sc), randn((I, H), s + 10, scale=I ** -0.5)]
+        self.we = [randn((E, H, I), s + 5, scale=sc), randn((E, H, I), s + 6, scale=sc),
+                   randn((E, I, H), s + 7, scale=I ** -0.5)]
+        self.wsh = [randn((H, I), s + 8, scale=sc), randn((H, I), s + 9, scale=sc),
+                    randn((I, H), s + 10, scale=I ** -0.5)]
         self.p, self.rng = 0.1, (rng_state(71, 5), rng_state(71, 10 ** 6))
         prec = mok.MOK_MXFP8 if mx else mok.MOK_BF16
         self.ws = mok.get_workspace(mok.MoKConfig(minibatch_rows=64, ring_bytes=1 << 20, precision=prec), device=DEV,
@@ -54,9 +56,11 @@ class Block:
         dy = ge["dx"]
         gs = mok.ffn_backward(self.fws, n["y"], self.sw[1], h, dffn, addend=dy)
         dl = mok.route_backward(ids, w, ge["dtopk_w"], self.E)
-        gn = mok.add_rmsnorm_backward(gs["dx"], n["sum"], self.gamma, n["rstd"], dsum=self.dres, p=self.p, rng=self.rng[0])
-        return dict(out=out, sum=n["sum"], ids=ids, w=w, status=sched, dlogits=dl, dres=gn["dresidual"], dbranch=gn["dx"],
-                    dgamma=gn["dweight"], dwd=gs["dw_down"], dwg=gs["dw_gate"], dwu=gs["dw_up"], dwe=ge["dw_down"])
+        gn = mok.add_rmsnorm_backward(gs["dx"], n["sum"], self.gamma, n["rstd"], dsum=self.dres, p=self.p,
+                                      rng=self.rng[0])
+        return dict(out=out, sum=n["sum"], ids=ids, w=w, status=sched, dlogits=dl,
+                    dres=gn["dresidual"], dbranch=gn["dx"], dgamma=gn["dweight"],
+                    dwd=gs["dw_down"], dwg=gs["dw_gate"], dwu=gs["dw_up"], dwe=ge["dw_down"])
 
 
 @pytest.mark.parametrize("mx", [False, True])

@@ -62,7 +62,8 @@ class Case:
 
     def oracle(self):
         f = host_f64
-        return dict(x=f(self.x), wg=f(self.wg), wu=f(self.wu), wd=f(self.wd), addend=None if self.add is None else f(self.add))
+        return dict(x=f(self.x), wg=f(self.wg), wu=f(self.wu), wd=f(self.wd),
+                    addend=None if self.add is None else f(self.add))
 
 
 def within(got, ref, tol, what):
@@ -257,6 +258,43 @@ def test_repeats_streams_and_graphs_give_the_same_bits(mx, T):
         torch.cuda.synchronize()
         for n, t in ref.items():
             assert torch.equal(got[n], t), (rep, n)
+
+
+@pytest.mark.parametrize("T", [1, 2])
+def test_block_scales_far_apart(T):
+    # 2^100 taken from the weights' scales and given to the rows': the same products
+    c = Case(T, 1024, 512, True, 65)
+    out, h = c.forward()
+    e, s = c.rows
+    q = c.keep
+    assert int(s.max()) <= 154 and int(q.fwd_gate[1].min()) >= 101 and int(q.fwd_up[1].min()) >= 101
+    w = mok.weights_mxfp8((q.fwd_gate[0], q.fwd_gate[1] - 100), (q.fwd_up[0], q.fwd_up[1] - 100), q.fwd_down, "fwd")
+    out2, h2 = mok.ffn_forward(c.ws, (e, s + 100), w, addend=c.add)
+    assert torch.equal(h, h2) and torch.equal(out, out2)
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("T", [1, 65, 520])
+def test_two_streams_at_once(mx, T):
+    # each with its own workspace, beside each other with no wait between them
+    a, b = Case(T, 1024, 512, mx, 66), Case(T, 1024, 512, mx, 67)
+    want = []
+    for c in (a, b):
+        out, h = c.forward()
+        want.append(dict(out=out, h=h, **c.backward(h)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(10):
+        for c, s, g in zip((a, b), streams, got):
+            with torch.cuda.stream(s):
+                out, h = c.forward()
+                g.append(dict(out=out, h=h, **c.backward(h)))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        for r in g:
+            for n, t in w.items():
+                assert torch.equal(r[n], t), n
 
 
 @pytest.mark.parametrize("H,I", [(64, 1 << 20), (1 << 20, 64)])

@@ -224,7 +224,8 @@ def test_repeats_streams_and_graphs_give_the_same_bits():
 
     def step(outs=None, grads=None):
         r = mok.add_rmsnorm(x, w, EPS, residual=res, p=p, rng=rng, mxfp8=True, outs=outs)
-        return r, mok.add_rmsnorm_backward(dy, r["sum"], w, r["rstd"], dsum=de, p=p, rng=rng, grads=grads, workspace=need)
+        return r, mok.add_rmsnorm_backward(dy, r["sum"], w, r["rstd"], dsum=de, p=p, rng=rng, grads=grads,
+                                           workspace=need)
 
     r0, g0 = step()
     s = torch.cuda.Stream()
