@@ -28,6 +28,8 @@ struct Span {
     const void *p;
     size_t n;
 };
+// The dropout state, where it is read.
+Span rng_span(float p, const uint64_t *rng) { return {p > 0.0f ? rng : nullptr, 16}; }
 bool overlap(Span a, Span b) {
     if (!a.p || !b.p || !a.n || !b.n) return false;
     const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
@@ -229,7 +231,8 @@ mok_status mok_dropout(const void *x, const void *residual, int64_t n, float p, 
     if (!dev_ok(x) || !dev_ok_or_null(residual) || !dev_ok(out)) return MOK_ERROR_INVALID_VALUE;
     const bool f32 = stream_dtype == MOK_STREAM_F32;
     const size_t sb = (size_t)n * (f32 ? 4 : 2);
-    if (overlap_partly({out, sb}, {residual, sb}) || overlap_partly({out, sb}, {x, (size_t)n * 2}))
+    if (overlap_partly({out, sb}, {residual, sb}) || overlap_partly({out, sb}, {x, (size_t)n * 2}) ||
+        overlap({out, sb}, rng_span(p, rng)))
         return MOK_ERROR_INVALID_VALUE;
     (void)hipGetLastError();
     return launch_dropout(static_cast<const uint16_t *>(x), residual, n, p, rng, f32, out,
@@ -242,7 +245,9 @@ mok_status mok_dropout_backward(const void *dy, int64_t n, float p, const uint64
     if (n == 0) return MOK_OK;
     if (!dev_ok(dy) || !dev_ok(dx)) return MOK_ERROR_INVALID_VALUE;
     const bool f32 = stream_dtype == MOK_STREAM_F32;
-    if (overlap_partly({dx, (size_t)n * 2}, {dy, (size_t)n * (f32 ? 4 : 2)})) return MOK_ERROR_INVALID_VALUE;
+    const Span sdx{dx, (size_t)n * 2};
+    if (overlap_partly(sdx, {dy, (size_t)n * (f32 ? 4 : 2)}) || overlap(sdx, rng_span(p, rng)))
+        return MOK_ERROR_INVALID_VALUE;
     (void)hipGetLastError();
     return launch_dropout_backward(dy, n, p, rng, f32, static_cast<uint16_t *>(dx), static_cast<hipStream_t>(stream));
 }
@@ -266,7 +271,8 @@ mok_status mok_add_rmsnorm(const mok_norm_shape *shape, const void *x, const voi
     const bool f32 = shape->stream_dtype == MOK_STREAM_F32;
     const Span sx{x, n * 2}, sr{residual, n * (f32 ? 4 : 2)}, ss{sum, n * (f32 ? 4 : 2)};
     const Span rest[] = {{y, n * 2}, {y_elems, n}, {y_scales, n / 32}, {rstd, (size_t)shape->T * 4}};
-    const Span outs[] = {ss, rest[0], rest[1], rest[2], rest[3]}, ins[] = {sx, sr, {weight, h2}, {rng, 16}};
+    const Span outs[] = {ss, rest[0], rest[1], rest[2], rest[3]};
+    const Span ins[] = {sx, sr, {weight, h2}, rng_span(shape->p, rng)};
     if (!apart(outs) || overlap_partly(ss, sx) || overlap_partly(ss, sr) || overlap(ss, ins[2]) || overlap(ss, ins[3]))
         return MOK_ERROR_INVALID_VALUE;
     for (const Span &o : rest)
@@ -312,7 +318,8 @@ mok_status mok_add_rmsnorm_backward(const mok_norm_shape *shape, void *workspace
     const bool f32 = shape->stream_dtype == MOK_STREAM_F32;
     const size_t sb = n * (f32 ? 4 : 2);
     const Span sres{dresidual, sb}, sdx{dx, n * 2}, sdw{dweight, 2 * h2}, sws{workspace, need};
-    const Span sdy{dy, n * 2}, sds{dsum, sb}, sin{sum, sb}, sw{weight, h2}, sr{rstd, (size_t)shape->T * 4}, sg{rng, 16};
+    const Span sdy{dy, n * 2}, sds{dsum, sb}, sin{sum, sb}, sw{weight, h2}, sr{rstd, (size_t)shape->T * 4};
+    const Span sg = rng_span(shape->p, rng);
     const Span outs[] = {sres, sdx, sdw, sws}, ins[] = {sdy, sds, sin, sw, sr, sg}, fixed[] = {sin, sw, sr, sg};
     if (!apart(outs) || any_overlap(sres, fixed) || any_overlap(sdx, fixed) || any_overlap(sdw, ins) ||
         any_overlap(sws, ins) || overlap(sres, sdy) || overlap_partly(sres, sds) || overlap(sdx, sds) ||

@@ -28,7 +28,7 @@ def _dropout(**over):
 @pytest.mark.parametrize("over", [dict(n=-1), dict(n=1 << 40), dict(p=1.0), dict(p=-0.1), dict(p=float("nan")),
                                   dict(rng=None), dict(rng=_a(2) + 4), dict(dtype=2), dict(dtype=-1), dict(x=None),
                                   dict(x=_a(0) + 2), dict(residual=_a(1) + 8), dict(out=None), dict(out=_a(3) + 1),
-                                  dict(out=_a(0) + 16), dict(out=_a(1) - 16),
+                                  dict(out=_a(0) + 16), dict(out=_a(1) - 16), dict(out=_a(2)), dict(out=_a(2) - 192),
                                   dict(dtype=mok.MOK_STREAM_F32, out=_a(0))])   # fp32 rows over the bf16 branch
 def test_dropout_refuses(over):
     assert _dropout(**over) == BAD
@@ -39,7 +39,7 @@ def test_dropout_of_nothing_is_a_no_op():
 
 
 @pytest.mark.parametrize("over", [dict(n=-1), dict(p=1.0), dict(rng=None), dict(dtype=3), dict(dy=None), dict(dx=None),
-                                  dict(dx=_a(0) + 32), dict(dtype=mok.MOK_STREAM_F32, dx=_a(0))])
+                                  dict(dx=_a(0) + 32), dict(dx=_a(2)), dict(dtype=mok.MOK_STREAM_F32, dx=_a(0))])
 def test_dropout_backward_refuses(over):
     k = dict(dy=_a(0), n=100, p=0.5, rng=_a(2), dtype=mok.MOK_STREAM_BF16, dx=_a(3))
     k.update(over)
