@@ -61,23 +61,38 @@ struct Fp8Stage {
 // A full chunk spans CB / 2 >= 2 stages; only the last chunk of the first
 // source (a W operand switching arrays) can be shorter, at least 1 stage,
 // and never two of those in a row: 2 + 1 >= 3.
-struct ScaleChunk {
-    uint32_t seq, pos;   // chunk number, and block of the stage's first 32-block inside it
+//
+// Stages are taken in order, by the loads and by the reads, so each keeps a
+// cursor that moves one stage at a time. (Worked out from the stage number
+// instead, a chunk costs a division by its length, 16 or 4: some 50 dependent
+// scalar instructions ahead of each stage's fragment reads.)
+template <class C>
+struct ScaleCursor {
+    uint32_t pos, buf;   // block of the stage's first 32-block inside its chunk; offset of the chunk's buffer
+    // From stage kt to the next: a chunk ends when it is full, and where the source changes (K = ksplit; 0: nowhere).
+    __device__ __forceinline__ void next(int kt, int cb, int ksplit) {
+        using S = Fp8Stage<C>;
+        pos += 2;
+        if (pos == (uint32_t)cb || (kt + 1) * S::BK8 == ksplit) {
+            pos = 0;
+            buf = buf == (S::NSCBUF - 1) * S::SCBUF_BYTES ? 0 : buf + S::SCBUF_BYTES;
+        }
+    }
 };
 template <class C>
 struct ScaleLoader {
     rsrc_t res, res2;
     uint32_t voff;   // byte offset of the lane's row in its source
-    int ksplit;      // K (elements) from which res2 holds the blocks, at K - ksplit
+    int ksplit;      // K (elements, whole stages) from which res2 holds the W blocks, at K - ksplit; 0: none
     int cbx, cbw;    // blocks per chunk of the X and the W operand (16 or 4)
-    int nq0w;        // W chunks of source 0 (before ksplit)
+    ScaleCursor<C> own;   // the next stage's loads, of the operand whose rows this wave loads
 
     // x/w: scale rows of the X / W operand ([rows][kbx or kbw] bytes, kb = K/32
     // of that array), nx/nw valid rows. w_hi: W rows [BN/2, BN) come from w_hi
     // instead (row - BN/2), each half with nw valid rows. w2: W blocks for
     // K >= wsplit come from w2, at K - wsplit.
     __device__ void init(const uint8_t *x, int nx, int kbx, const uint8_t *w, int nw, int kbw,
-                         const uint8_t *w_hi = nullptr, const uint8_t *w2 = nullptr, int wsplit = 1 << 30) {
+                         const uint8_t *w_hi = nullptr, const uint8_t *w2 = nullptr, int wsplit = 0) {
         const int wave = wave_id(), L = threadIdx.x & 63;
         const bool is_w = wave >= 4;
         int r = (wave & 3) * 64 + L;
@@ -95,46 +110,33 @@ struct ScaleLoader {
         const uint32_t bytes = (uint32_t)((int64_t)max(n, 0) * kb);
         res = make_rsrc(base, bytes);
         res2 = make_rsrc(is_w && w2 ? w2 : base, bytes);
-        ksplit = w2 ? wsplit : (1 << 30);
+        ksplit = w2 ? wsplit : 0;
         voff = (uint32_t)r * (uint32_t)kb;
         // 16-byte chunks where every row of every source starts 16-byte aligned
         auto a16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
         cbx = (kbx % 16 == 0 && a16(x)) ? 16 : 4;
         cbw = (kbw % 16 == 0 && a16(w) && (!w_hi || a16(w_hi)) && (!w2 || a16(w2))) ? 16 : 4;
-        nq0w = w2 ? (wsplit / 32 + cbw - 1) / cbw : 0;
+        own = ScaleCursor<C>{0, 0};
     }
-    __device__ __forceinline__ ScaleChunk chunk_x(int kt) const {
-        const uint32_t b = (uint32_t)kt * 2u;
-        return ScaleChunk{b / (uint32_t)cbx, b % (uint32_t)cbx};
-    }
-    __device__ __forceinline__ ScaleChunk chunk_w(int kt) const {
-        const int k0 = kt * Fp8Stage<C>::BK8;
-        if (k0 < ksplit) {
-            const uint32_t b = (uint32_t)k0 / 32u;
-            return ScaleChunk{b / (uint32_t)cbw, b % (uint32_t)cbw};
-        }
-        const uint32_t b = (uint32_t)(k0 - ksplit) / 32u;
-        return ScaleChunk{(uint32_t)nq0w + b / (uint32_t)cbw, b % (uint32_t)cbw};
-    }
-    // LDS address of chunk c's buffer for the X (w = false) or W operand
-    static __device__ __forceinline__ uint32_t buffer(uint32_t lds, bool w, uint32_t seq) {
-        return lds + (uint32_t)Fp8Stage<C>::SC_OFF +
-               ((w ? (uint32_t)Fp8Stage<C>::NSCBUF : 0u) + seq % (uint32_t)Fp8Stage<C>::NSCBUF) *
-                   (uint32_t)Fp8Stage<C>::SCBUF_BYTES;
+    // LDS address of the X (w = false) or W operand's chunk buffers
+    static __device__ __forceinline__ uint32_t buffers(uint32_t lds, bool w) {
+        using S = Fp8Stage<C>;
+        return lds + (uint32_t)S::SC_OFF + (w ? (uint32_t)(S::NSCBUF * S::SCBUF_BYTES) : 0u);
     }
     // Before the operand loads of stage kt: this wave's rows of the chunk that
     // starts at kt, if one does. lds: the tile's LDS base.
-    __device__ void issue(int kt, uint32_t lds) const {
+    __device__ void issue(int kt, uint32_t lds) {
         const bool is_w = wave_id() >= 4;
-        const ScaleChunk c = is_w ? chunk_w(kt) : chunk_x(kt);
-        if (c.pos != 0) return;
-        const int cb = is_w ? cbw : cbx;
-        const int k0 = kt * Fp8Stage<C>::BK8;
-        const bool second = is_w && k0 >= ksplit;
-        const uint32_t soff = (uint32_t)((second ? k0 - ksplit : k0) >> 5);   // first block of the chunk
-        const uint32_t dst = buffer(lds, is_w, c.seq) + (uint32_t)((wave_id() & 3) * 64 * cb);
-        if (cb == 16) load_lds16(second ? res2 : res, voff, soff, dst);
-        else load_lds4(second ? res2 : res, voff, soff, dst);
+        const int cb = is_w ? cbw : cbx, split = is_w ? ksplit : 0;
+        if (own.pos == 0) {
+            const int k0 = kt * Fp8Stage<C>::BK8;
+            const bool second = split != 0 && k0 >= split;
+            const uint32_t soff = (uint32_t)((second ? k0 - split : k0) >> 5);   // first block of the chunk
+            const uint32_t dst = buffers(lds, is_w) + own.buf + (uint32_t)((wave_id() & 3) * 64 * cb);
+            if (cb == 16) load_lds16(second ? res2 : res, voff, soff, dst);
+            else load_lds4(second ? res2 : res, voff, soff, dst);
+        }
+        own.next(kt, cb, split);
     }
 };
 
@@ -186,20 +188,24 @@ __device__ __forceinline__ uint64_t gemm8_tile(P &p, uint32_t lds, F &&between, 
 
     i32x8_t wa[FN], xb[FM];
     int swa[FN], sxb[FM];
-    auto read_stage = [&](int kt) {
+    ScaleCursor<C> cw{0, 0}, cx{0, 0};
+    const int cbw = p.sl.cbw, cbx = p.sl.cbx, ksplit = p.sl.ksplit;
+    auto read_stage = [&](int kt) {   // stages in order
         const uint32_t st = stage(kt);
-        const ScaleChunk cw = p.sl.chunk_w(kt), cx = p.sl.chunk_x(kt);
-        const uint32_t bw = ScaleLoader<C>::buffer(lds, true, cw.seq), bx = ScaleLoader<C>::buffer(lds, false, cx.seq);
+        const uint32_t bw = ScaleLoader<C>::buffers(lds, true) + cw.buf;
+        const uint32_t bx = ScaleLoader<C>::buffers(lds, false) + cx.buf;
 #pragma unroll
         for (int fn = 0; fn < FN; ++fn) {
             wa[fn] = frag8(st + C::X_BYTES, p.wrow(wn, fn));
-            swa[fn] = scale8(bw, p.sl.cbw, cw.pos, p.wrow(wn, fn));
+            swa[fn] = scale8(bw, cbw, cw.pos, p.wrow(wn, fn));
         }
 #pragma unroll
         for (int fm = 0; fm < FM; ++fm) {
             xb[fm] = frag8(st, wm * C::WM + fm * 32);
-            sxb[fm] = scale8(bx, p.sl.cbx, cx.pos, wm * C::WM + fm * 32);
+            sxb[fm] = scale8(bx, cbx, cx.pos, wm * C::WM + fm * 32);
         }
+        cw.next(kt, cbw, ksplit);
+        cx.next(kt, cbx, 0);
     };
     // The empty asm after each MFMA takes its accumulator as an operand, which
     // pins the MFMA phase where the schedule puts it. Without it the compiler
