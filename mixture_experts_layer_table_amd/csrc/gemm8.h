@@ -62,20 +62,36 @@ struct Fp8Stage {
 // source (a W operand switching arrays) can be shorter, at least 1 stage,
 // and never two of those in a row: 2 + 1 >= 3.
 //
-// Stages are taken in order, by the loads and by the reads, so each keeps a
-// cursor that moves one stage at a time. (Worked out from the stage number
-// instead, a chunk costs a division by its length, 16 or 4: some 50 dependent
-// scalar instructions ahead of each stage's fragment reads.)
+// Stages are taken in order, by the loads and by the reads, so both follow the
+// chunks with a counter that is touched once a chunk. (Worked out from the
+// stage number instead, a chunk costs a division by its length, 16 or 4: some
+// 50 dependent scalar instructions ahead of each stage's fragment reads.)
 template <class C>
 struct ScaleCursor {
-    uint32_t pos, buf;   // block of the stage's first 32-block inside its chunk; offset of the chunk's buffer
-    // From stage kt to the next: a chunk ends when it is full, and where the source changes (K = ksplit; 0: nowhere).
-    __device__ __forceinline__ void next(int kt, int cb, int ksplit) {
+    uint32_t off;    // offset of the next stage's first block in the operand's chunk buffers
+    int end, span;   // the stage that starts the next chunk; stages in a full chunk
+    int split;       // the stage at which the source changes, which also starts a chunk (kNoSplit: none)
+    static constexpr int kNoSplit = 1 << 30;
+
+    __device__ __forceinline__ static int chunk_end(int kt, int span, int split) {
+        return kt < split ? min(kt + span, split) : kt + span;
+    }
+    __device__ __forceinline__ static uint32_t next_buffer(uint32_t buf) {
         using S = Fp8Stage<C>;
-        pos += 2;
-        if (pos == (uint32_t)cb || (kt + 1) * S::BK8 == ksplit) {
-            pos = 0;
-            buf = buf == (S::NSCBUF - 1) * S::SCBUF_BYTES ? 0 : buf + S::SCBUF_BYTES;
+        return buf == (uint32_t)((S::NSCBUF - 1) * S::SCBUF_BYTES) ? 0u : buf + (uint32_t)S::SCBUF_BYTES;
+    }
+    __device__ __forceinline__ void start(int span_, int split_) {
+        off = 0;
+        span = span_;
+        split = split_;
+        end = chunk_end(0, span, split);
+    }
+    __device__ __forceinline__ void next(int kt) {   // from stage kt to stage kt + 1
+        off += 2;
+        if (__builtin_expect(kt + 1 == end, 0)) {
+            asm volatile("");   // keeps this a branch: selects would cost every stage its instructions
+            off = next_buffer(off & ~(uint32_t)(Fp8Stage<C>::SCBUF_BYTES - 1));
+            end = chunk_end(end, span, split);
         }
     }
 };
@@ -83,16 +99,19 @@ template <class C>
 struct ScaleLoader {
     rsrc_t res, res2;
     uint32_t voff;   // byte offset of the lane's row in its source
-    int ksplit;      // K (elements, whole stages) from which res2 holds the W blocks, at K - ksplit; 0: none
     int cbx, cbw;    // blocks per chunk of the X and the W operand (16 or 4)
-    ScaleCursor<C> own;   // the next stage's loads, of the operand whose rows this wave loads
+    int wsplit;      // stage from which the W operand's blocks come from its second array
+    // this wave's loads: blocks per chunk and split of its operand, the stage
+    // of its next chunk, that chunk's buffer, and the wave's place in a buffer
+    int cb, split, at;
+    uint32_t buf, dst0;
 
     // x/w: scale rows of the X / W operand ([rows][kbx or kbw] bytes, kb = K/32
     // of that array), nx/nw valid rows. w_hi: W rows [BN/2, BN) come from w_hi
     // instead (row - BN/2), each half with nw valid rows. w2: W blocks for
-    // K >= wsplit come from w2, at K - wsplit.
+    // K >= wsplit_k (whole stages) come from w2, at K - wsplit_k.
     __device__ void init(const uint8_t *x, int nx, int kbx, const uint8_t *w, int nw, int kbw,
-                         const uint8_t *w_hi = nullptr, const uint8_t *w2 = nullptr, int wsplit = 0) {
+                         const uint8_t *w_hi = nullptr, const uint8_t *w2 = nullptr, int wsplit_k = 0) {
         const int wave = wave_id(), L = threadIdx.x & 63;
         const bool is_w = wave >= 4;
         int r = (wave & 3) * 64 + L;
@@ -110,13 +129,17 @@ struct ScaleLoader {
         const uint32_t bytes = (uint32_t)((int64_t)max(n, 0) * kb);
         res = make_rsrc(base, bytes);
         res2 = make_rsrc(is_w && w2 ? w2 : base, bytes);
-        ksplit = w2 ? wsplit : 0;
+        wsplit = w2 ? wsplit_k / Fp8Stage<C>::BK8 : ScaleCursor<C>::kNoSplit;
         voff = (uint32_t)r * (uint32_t)kb;
         // 16-byte chunks where every row of every source starts 16-byte aligned
         auto a16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
         cbx = (kbx % 16 == 0 && a16(x)) ? 16 : 4;
         cbw = (kbw % 16 == 0 && a16(w) && (!w_hi || a16(w_hi)) && (!w2 || a16(w2))) ? 16 : 4;
-        own = ScaleCursor<C>{0, 0};
+        cb = is_w ? cbw : cbx;
+        split = is_w ? wsplit : ScaleCursor<C>::kNoSplit;
+        at = 0;
+        buf = 0;
+        dst0 = buffers(0, is_w) + (uint32_t)((wave & 3) * 64 * cb);
     }
     // LDS address of the X (w = false) or W operand's chunk buffers
     static __device__ __forceinline__ uint32_t buffers(uint32_t lds, bool w) {
@@ -125,18 +148,15 @@ struct ScaleLoader {
     }
     // Before the operand loads of stage kt: this wave's rows of the chunk that
     // starts at kt, if one does. lds: the tile's LDS base.
-    __device__ void issue(int kt, uint32_t lds) {
-        const bool is_w = wave_id() >= 4;
-        const int cb = is_w ? cbw : cbx, split = is_w ? ksplit : 0;
-        if (own.pos == 0) {
-            const int k0 = kt * Fp8Stage<C>::BK8;
-            const bool second = split != 0 && k0 >= split;
-            const uint32_t soff = (uint32_t)((second ? k0 - split : k0) >> 5);   // first block of the chunk
-            const uint32_t dst = buffers(lds, is_w) + own.buf + (uint32_t)((wave_id() & 3) * 64 * cb);
-            if (cb == 16) load_lds16(second ? res2 : res, voff, soff, dst);
-            else load_lds4(second ? res2 : res, voff, soff, dst);
-        }
-        own.next(kt, cb, split);
+    __device__ __forceinline__ void issue(int kt, uint32_t lds) {
+        if (__builtin_expect(kt != at, 1)) return;
+        const bool second = kt >= split;
+        const uint32_t soff = (uint32_t)((second ? kt - split : kt) * 2);   // first block of the chunk
+        const uint32_t dst = lds + dst0 + buf;
+        if (cb == 16) load_lds16(second ? res2 : res, voff, soff, dst);
+        else load_lds4(second ? res2 : res, voff, soff, dst);
+        buf = ScaleCursor<C>::next_buffer(buf);
+        at = ScaleCursor<C>::chunk_end(kt, cb / 2, split);
     }
 };
 
@@ -149,8 +169,8 @@ __device__ __forceinline__ i32x8_t frag8(uint32_t tile, int row) {
     return i32x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 }
 
-// Scale byte of (tile row `row` + l%32, block l/32 of the stage) from the
-// chunk buffer `buf` of CB-byte rows, the stage's first block at `pos`.
+// Scale byte of (tile row `row` + l%32, block l/32 of the stage) from an
+// operand's chunk buffers of cb-byte rows, the stage's first block at `pos`.
 __device__ __forceinline__ int scale8(uint32_t buf, int cb, uint32_t pos, int row) {
     const int l = threadIdx.x & 63;
     const uint32_t a = buf + (uint32_t)((row + (l & 31)) * cb) + pos + (uint32_t)(l >> 5);
@@ -188,24 +208,25 @@ __device__ __forceinline__ uint64_t gemm8_tile(P &p, uint32_t lds, F &&between, 
 
     i32x8_t wa[FN], xb[FM];
     int swa[FN], sxb[FM];
-    ScaleCursor<C> cw{0, 0}, cx{0, 0};
-    const int cbw = p.sl.cbw, cbx = p.sl.cbx, ksplit = p.sl.ksplit;
+    ScaleCursor<C> cw, cx;
+    const int cbw = p.sl.cbw, cbx = p.sl.cbx;
+    cw.start(cbw / 2, p.sl.wsplit);
+    cx.start(cbx / 2, ScaleCursor<C>::kNoSplit);
+    const uint32_t bw = ScaleLoader<C>::buffers(lds, true), bx = ScaleLoader<C>::buffers(lds, false);
     auto read_stage = [&](int kt) {   // stages in order
         const uint32_t st = stage(kt);
-        const uint32_t bw = ScaleLoader<C>::buffers(lds, true) + cw.buf;
-        const uint32_t bx = ScaleLoader<C>::buffers(lds, false) + cx.buf;
 #pragma unroll
         for (int fn = 0; fn < FN; ++fn) {
             wa[fn] = frag8(st + C::X_BYTES, p.wrow(wn, fn));
-            swa[fn] = scale8(bw, cbw, cw.pos, p.wrow(wn, fn));
+            swa[fn] = scale8(bw, cbw, cw.off, p.wrow(wn, fn));
         }
 #pragma unroll
         for (int fm = 0; fm < FM; ++fm) {
             xb[fm] = frag8(st, wm * C::WM + fm * 32);
-            sxb[fm] = scale8(bx, cbx, cx.pos, wm * C::WM + fm * 32);
+            sxb[fm] = scale8(bx, cbx, cx.off, wm * C::WM + fm * 32);
         }
-        cw.next(kt, cbw, ksplit);
-        cx.next(kt, cbx, 0);
+        cw.next(kt);
+        cx.next(kt);
     };
     // The empty asm after each MFMA takes its accumulator as an operand, which
     // pins the MFMA phase where the schedule puts it. Without it the compiler
@@ -233,26 +254,47 @@ __device__ __forceinline__ uint64_t gemm8_tile(P &p, uint32_t lds, F &&between, 
         else wait_vmcnt<0>();
         lds_barrier();
     }
+    // The loop proper, whose waits are constants, then its last stages, which
+    // have nothing left to load.
+    const int steady = max(nk - 3, 0);
     if (wm == 0) {
         if (nk > 0) read_stage(0);
-        for (int kt = 0; kt < nk; ++kt) {
+        int kt = 0;
+        for (; kt < steady; ++kt) {
+            __builtin_amdgcn_sched_barrier(0);
+            mma_stage();
+            __builtin_amdgcn_sched_barrier(0);
+            wait_vmcnt<L>();
+            lds_barrier();
+            p.issue(kt + 3, stage(kt + 3));
+            read_stage(kt + 1);
+        }
+        for (; kt < nk; ++kt) {
             __builtin_amdgcn_sched_barrier(0);
             mma_stage();
             __builtin_amdgcn_sched_barrier(0);
             if (kt + 2 < nk) wait_vmcnt<L>();
             else wait_vmcnt<0>();
             lds_barrier();
-            if (kt + 3 < nk) p.issue(kt + 3, stage(kt + 3));
             if (kt + 1 < nk) read_stage(kt + 1);
         }
     } else {
-        for (int kt = 0; kt < nk; ++kt) {
-            if (kt + 3 < nk) p.issue(kt + 3, stage(kt + 3));
+        int kt = 0;
+        for (; kt < steady; ++kt) {
+            p.issue(kt + 3, stage(kt + 3));
             read_stage(kt);
-            if (kt + 3 < nk) wait_vmcnt<2 * L>();
-            else if (kt + 2 < nk) wait_vmcnt<L>();
-            else wait_vmcnt<0>();
+            wait_vmcnt<2 * L>();
             wait_lgkm0();   // fragment reads of stage kt landed: the slot is refilled right after this barrier
+            lds_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            mma_stage();
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        for (; kt < nk; ++kt) {
+            read_stage(kt);
+            if (kt + 2 < nk) wait_vmcnt<L>();
+            else wait_vmcnt<0>();
+            wait_lgkm0();
             lds_barrier();
             __builtin_amdgcn_sched_barrier(0);
             mma_stage();
