@@ -266,8 +266,8 @@ __device__ __forceinline__ uint64_t gemm8_tile(P &p, uint32_t lds, F &&between, 
             __builtin_amdgcn_sched_barrier(0);
             wait_vmcnt<L>();
             lds_barrier();
-            p.issue(kt + 3, stage(kt + 3));
             read_stage(kt + 1);
+            p.issue(kt + 3, stage(kt + 3));
         }
         for (; kt < nk; ++kt) {
             __builtin_amdgcn_sched_barrier(0);
@@ -281,8 +281,8 @@ __device__ __forceinline__ uint64_t gemm8_tile(P &p, uint32_t lds, F &&between, 
     } else {
         int kt = 0;
         for (; kt < steady; ++kt) {
-            p.issue(kt + 3, stage(kt + 3));
             read_stage(kt);
+            p.issue(kt + 3, stage(kt + 3));
             wait_vmcnt<2 * L>();
             wait_lgkm0();   // fragment reads of stage kt landed: the slot is refilled right after this barrier
             lds_barrier();
