@@ -42,7 +42,7 @@ FfnSplit choose(int64_t T, int64_t N, int64_t n_tiles, int steps, bool mx) {
     FfnSplit best{256, 1, steps};
     double least = 1e30;
     for (int bm : {256, 128}) {
-        const double step_us = bm == 256 ? (mx ? 0.85 : 0.75) : (mx ? 0.74 : 0.5);
+        const double step_us = bm == 256 ? (mx ? 0.8 : 0.75) : (mx ? 0.53 : 0.5);
         const int64_t tiles = ceil_div(T, bm) * n_tiles;
         for (int s = 1; s <= kMaxSplits; ++s) {
             int len = (int)ceil_div(steps, s);
