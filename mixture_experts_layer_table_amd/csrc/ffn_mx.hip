@@ -8,13 +8,13 @@
 // h, the outputs and the weight gradients are BF16, as in ffn.hip, whose
 // formulas and split over the contraction axis this file shares.
 //
-// Measured: forward 2,048 x 7,168 x 2,048 126 us (1,435 TFLOP/s; its gate/up
-// product has 128 tiles of 256 rows for 256 compute units, so it is cut in two
-// and joined in 16 us), 16,384 rows 0.73 ms (1,990); backward 16,384 rows
-// 1.97 ms, of which the BF16 weight gradients are half the flops. A 128-row tile
-// takes 0.74 us a K-step where the 256-row one takes 0.85 (its four MFMAs a step
-// do not cover the barrier and the fragment reads; a fifth ring stage changed
-// nothing), so it only pays where it saves a split.
+// Measured: forward 2,048 x 7,168 x 2,048 115 us (1,570 TFLOP/s; its gate/up
+// product has 128 tiles of 256 rows for 256 compute units: 128-row tiles instead,
+// 71 us, where 256 rows cut in two take 62 and their join 15), 16,384 rows
+// 0.70 ms (2,060); backward 16,384 rows 1.91 ms, of which the BF16 weight
+// gradients are half the flops. A 128-row tile takes 0.5 to 0.6 us a K-step where
+// the 256-row one takes 0.8 (its four MFMAs a step, 0.2 us, do not cover the
+// barrier and the fragment reads), so it pays where it saves a split or a round.
 #include "ffn_parts.h"
 #include "gemm8.h"
 #include "kernels.h"
@@ -223,7 +223,7 @@ struct FfnDA8 : Ffn8Base<Cfg> {
     // As the BF16 dA: h rows come in and dh and a rows leave as whole row runs,
     // staged one 32-row fragment at a time through row descriptors; dh's codes
     // take a fourth staging array, their scales one 2-byte store a row and half.
-    // (At 16,384 x 7,168 x 2,048: 315 us; 411 with each lane's pieces stored
+    // (At 16,384 x 7,168 x 2,048: 307 us; 411 with each lane's pieces stored
     // directly and quantized out of line, every call waiting for all stores in
     // flight. The tiles write and read 400 MB in two bursts, 78 us of HBM time.)
     __device__ void epilogue(f32x16_t (&acc)[C::FM][C::FN], int wm, int wn) {

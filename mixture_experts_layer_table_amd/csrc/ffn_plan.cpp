@@ -35,7 +35,7 @@ size_t part_bytes(int64_t T, int H, int I) {
 // from the rounds of tiles over the compute units, the time of a K-step, and
 // the join with its partials' traffic. The constants were fitted to kernel
 // traces of 15 lengths from 3 to 4,096 rows at 7,168 x 2,048, 4,096 x 1,024,
-// 2,048 x 768, 1,024 x 512 and 512 x 2,048: the choices are 1.4% slower than the
+// 2,048 x 768, 1,024 x 512 and 512 x 2,048: the choices are 1.5% slower than the
 // best measured ones in the mean, 25% at most.
 // Depends on the shape alone, so the bits of a result do too.
 FfnSplit choose(int64_t T, int64_t N, int64_t n_tiles, int steps, bool mx) {
@@ -62,9 +62,9 @@ FfnSplit choose(int64_t T, int64_t N, int64_t n_tiles, int steps, bool mx) {
 }
 
 // The few-rows forward, where it is faster than the tiles (GPU time of a call):
-// one row always (7,168 x 2,048 BF16 24 us against 28, MXFP8 14 against 26;
-// 1,024 x 512 12 against 16 and 7 against 16); two rows in MXFP8 (20 against 26,
-// 10 against 16) and in BF16 up to 2^23 weights a matrix (4,096 x 1,024 19 us
+// one row always (7,168 x 2,048 BF16 24 us against 28, MXFP8 16 against 24;
+// 1,024 x 512 12 against 16 and 7 against 15); two rows in MXFP8 (20 against 24,
+// 10 against 15) and in BF16 up to 2^23 weights a matrix (4,096 x 1,024 19 us
 // against 24; 7,168 x 2,048 32 against 29). Its buffers in LDS stay under
 // 64 KiB (the rows of a in fp32), and BF16 cuts the gate/up product into at
 // most 16 runs of at most 2,048 rows, about one workgroup per compute unit.

@@ -255,7 +255,8 @@ __device__ __forceinline__ uint64_t gemm8_tile(P &p, uint32_t lds, F &&between, 
         lds_barrier();
     }
     // The loop proper, whose waits are constants, then its last stages, which
-    // have nothing left to load.
+    // have nothing left to load. The fragment reads go out ahead of the stage's
+    // loads: the MFMAs wait for those, and the loads have three stages' time.
     const int steady = max(nk - 3, 0);
     if (wm == 0) {
         if (nk > 0) read_stage(0);

@@ -280,8 +280,8 @@ RowShape row_shape(int H, int64_t rows) {
 }
 
 // Workgroups of the backward: about kBwdWaves waves in all, each with an equal
-// number of rows. More shares cost their traffic (16,384 x 7,168: 181 us with
-// 384 workgroups, 192 with 1,024), fewer leave units idle (16,384 x 512: 55 us
+// number of rows. More shares cost their traffic (16,384 x 7,168: 182 us with
+// 432 workgroups, 192 with 1,024), fewer leave units idle (16,384 x 512: 55 us
 // with 256, 23 with 1,024).
 constexpr int kBwdWaves = 3000;
 int backward_target(int H, int64_t T) { return std::max(1, kBwdWaves / row_shape(H, T).waves); }
