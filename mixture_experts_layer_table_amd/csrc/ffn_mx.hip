@@ -11,10 +11,11 @@
 // Measured: forward 2,048 x 7,168 x 2,048 115 us (1,570 TFLOP/s; its gate/up
 // product has 128 tiles of 256 rows for 256 compute units: 128-row tiles instead,
 // 71 us, where 256 rows cut in two take 62 and their join 15), 16,384 rows
-// 0.70 ms (2,060); backward 16,384 rows 1.91 ms, of which the BF16 weight
+// 0.69 ms (2,100); backward 16,384 rows 1.88 ms, of which the BF16 weight
 // gradients are half the flops. A 128-row tile takes 0.5 to 0.6 us a K-step where
-// the 256-row one takes 0.8 (its four MFMAs a step, 0.2 us, do not cover the
-// barrier and the fragment reads), so it pays where it saves a split or a round.
+// the 256-row one takes 0.8, so it pays where it saves a split or a round. Both
+// wait for their operands (2,048 rows' gate/up: 68 us; 64 without the MFMAs, 49
+// without the loads, 68 without the fragment reads).
 #include "ffn_parts.h"
 #include "gemm8.h"
 #include "kernels.h"
@@ -73,12 +74,19 @@ struct Ffn8Base {
     Args a;
 
     // false: no tile; k0: the run's first value of a contraction axis of K values
+    template <bool TILED>
     __device__ bool begin(const Args &args, int b, int K, int &k0) {
         a = args;
         if (!ffn_tile(a.T, C::BM, a.n_tiles, a.splits, b, t)) return false;
         k0 = t.s * a.len * kK8;
         nk = min(a.len, K / kK8 - t.s * a.len);
-        xl.init(as_pairs(a.x + (int64_t)t.m0 * K + k0), K / 2, t.rows);
+        if constexpr (TILED) {
+            const uint32_t off = tiled_at((uint32_t)a.T, (uint32_t)t.m0, (uint32_t)k0);
+            xl.init_tiled(a.x + off, (uint32_t)a.T * 64u, (uint32_t)a.T * (uint32_t)K - off);
+            __builtin_assume(xl.kblock != 0);
+        } else {
+            xl.init(as_pairs(a.x + (int64_t)t.m0 * K + k0), K / 2, t.rows);
+        }
         return true;
     }
     __device__ const uint8_t *x_scales(int K, int k0) const { return a.xs + (int64_t)t.m0 * (K / 32) + k0 / 32; }
@@ -97,7 +105,6 @@ struct FfnGateUp8 : Ffn8Base<Cfg> {
     using typename B::C;
     using typename B::S8;
     using B::a;
-    using B::begin;
     using B::sl;
     using B::t;
     using B::wl;
@@ -106,7 +113,7 @@ struct FfnGateUp8 : Ffn8Base<Cfg> {
     __device__ bool setup(const Args &args, int b) {
         int k0;
         const int H = args.H;
-        if (!begin(args, b, H, k0)) return false;
+        if (!B::template begin<false>(args, b, H, k0)) return false;
         const int i0 = t.nt * (C::BN / 2), nw = min(C::BN / 2, a.I - i0);
         const int64_t wo = (int64_t)i0 * H + k0, so = (int64_t)i0 * (H / 32) + k0 / 32;
         wl.init_split_rows(as_pairs(a.w0 + wo), as_pairs(a.w1 + wo), H / 2, nw);
@@ -143,7 +150,8 @@ struct FfnGateUp8 : Ffn8Base<Cfg> {
         static_assert(C::FN == 2, "one gate and one up block of 32 columns per wave");
         const int lane = epi_lane();
         const uint32_t area = FS::area(wave_id(), 1);
-        const brsrc_t qres = rows_rsrc(a.q + (int64_t)t.m0 * I, (uint32_t)t.rows * (uint32_t)I);
+        const brsrc_t qres = rows_rsrc(a.q, (uint32_t)a.T * (uint32_t)I);
+        const uint32_t q0 = tiled_at((uint32_t)a.T, (uint32_t)t.m0, (uint32_t)(ib0 + (lane & 3) * 8));
         const brsrc_t sres = rows_rsrc(a.qs + (int64_t)t.m0 * (I / 32), (uint32_t)t.rows * (uint32_t)(I / 32));
 #pragma unroll
         for (int fm = 0; fm < C::FM; ++fm) {
@@ -160,7 +168,8 @@ struct FfnGateUp8 : Ffn8Base<Cfg> {
 #pragma unroll
             for (int p = 0; p < 2; ++p) {   // 16 rows a pass, 8 codes a lane
                 const int r = p * 16 + (lane >> 2);
-                bstore8_nt(qres, (m0 + (uint32_t)r) * (uint32_t)I + (uint32_t)(ib0 + (lane & 3) * 8), 0,
+                const uint32_t m = m0 + (uint32_t)r;
+                bstore8_nt(qres, m < (uint32_t)t.rows ? q0 + m * 64u : kOutOfRange, 0,
                            FS::get(area + FS::at(r, lane & 3)));
             }
             bstore1(sres, lane < 32 ? (m0 + (uint32_t)lane) * (uint32_t)(I / 32) + (uint32_t)(ib0 / 32) : kOutOfRange,
@@ -176,7 +185,6 @@ struct FfnDown8 : Ffn8Base<Cfg> {
     using typename B::C;
     using typename B::S8;
     using B::a;
-    using B::begin;
     using B::sl;
     using B::t;
     using B::wl;
@@ -185,7 +193,7 @@ struct FfnDown8 : Ffn8Base<Cfg> {
     __device__ bool setup(const Args &args, int b) {
         int k0;
         const int I = args.I;
-        if (!begin(args, b, I, k0)) return false;
+        if (!B::template begin<true>(args, b, I, k0)) return false;
         const int n0 = t.nt * C::BN, nw = min(C::BN, a.H - n0);
         wl.init(as_pairs(a.w0 + (int64_t)n0 * I + k0), I / 2, nw);
         sl.init(x_scales(I, k0), t.rows, I / 32, a.w0s + (int64_t)n0 * (I / 32) + k0 / 32, nw, I / 32);
@@ -203,7 +211,6 @@ struct FfnDA8 : Ffn8Base<Cfg> {
     using typename B::C;
     using typename B::S8;
     using B::a;
-    using B::begin;
     using B::sl;
     using B::t;
     using B::wl;
@@ -212,7 +219,7 @@ struct FfnDA8 : Ffn8Base<Cfg> {
     __device__ bool setup(const Args &args, int b) {
         int k0;
         const int H = args.H;
-        if (!begin(args, b, H, k0)) return false;
+        if (!B::template begin<true>(args, b, H, k0)) return false;
         const int i0 = t.nt * C::BN, nw = min(C::BN, a.I - i0);
         wl.init(as_pairs(a.w0 + (int64_t)i0 * H + k0), H / 2, nw);
         sl.init(x_scales(H, k0), t.rows, H / 32, a.w0s + (int64_t)i0 * (H / 32) + k0 / 32, nw, H / 32);
@@ -244,14 +251,15 @@ struct FfnDA8 : Ffn8Base<Cfg> {
         const brsrc_t hres = rows_rsrc(a.h_in + (int64_t)t.m0 * 2 * I, rows * row_bytes);
         const brsrc_t dres = rows_rsrc(a.dh + (int64_t)t.m0 * 2 * I, rows * row_bytes);
         const brsrc_t ares = rows_rsrc(a.a + (int64_t)t.m0 * I, rows * up);
-        const brsrc_t qres = rows_rsrc(a.q + (int64_t)t.m0 * 2 * I, rows * up);
+        const brsrc_t qres = rows_rsrc(a.q, (uint32_t)a.T * up);
         const brsrc_t sres = rows_rsrc(a.qs + (int64_t)t.m0 * sc_bytes, rows * sc_bytes);
         // the lane's byte offsets at pass 0 of fragment 0; pass p of fragment fm lies step(fm, p) rows further.
-        // A row's 128 staged code bytes are 64 of the gate half and 64 of the up half.
+        // A row's 128 staged code bytes are 64 of the gate half and 64 of the up half: one block of each.
         const uint32_t row0 = (uint32_t)(wm * C::WM + FS::pass_row(0, lane));
         const uint32_t d0 = row0 * row_bytes + 2u * (uint32_t)(ib + FS::pass_col(lane));
         const uint32_t a0 = row0 * up + 2u * (uint32_t)(ib + FS::pass_col(lane));
-        const uint32_t q0 = row0 * up + (uint32_t)(ib + (lane % 8) * 8 + (lane % 16 >= 8 ? I : 0));
+        const uint32_t q0 = tiled_at((uint32_t)a.T, (uint32_t)t.m0 + row0,
+                                     (uint32_t)(ib + (lane % 8) * 8 + (lane % 16 >= 8 ? I : 0)));
         auto step = [](int fm, int p) { return (uint32_t)(fm * 32 + p * FS::RPP); };
         uint2 hg[FS::PASSES], hu[FS::PASSES];
         auto load_h = [&](int fm) {
@@ -311,7 +319,7 @@ struct FfnDA8 : Ffn8Base<Cfg> {
                 bstore8_nt(dres, v, 0, FS::get(sg + o));
                 bstore8_nt(dres, v, up, FS::get(su + o));
                 bstore8_nt(ares, a0 + step(fm, p) * up, 0, FS::get(sa + o));
-                bstore8_nt(qres, q0 + step(fm, p) * up, 0, FS::get(sq + o));
+                bstore8_nt(qres, row0 + step(fm, p) < rows ? q0 + step(fm, p) * 64u : kOutOfRange, 0, FS::get(sq + o));
             }
             const uint32_t sr = (uint32_t)(wm * C::WM + fm * 32 + (lane & 31)) * sc_bytes;
             bstore2(sres, sr + (uint32_t)((ib + (lane < 32 ? 0 : I)) / 32), sc);
@@ -326,7 +334,6 @@ struct FfnDX8 : Ffn8Base<Cfg> {
     using typename B::C;
     using typename B::S8;
     using B::a;
-    using B::begin;
     using B::sl;
     using B::t;
     using B::wl;
@@ -335,7 +342,7 @@ struct FfnDX8 : Ffn8Base<Cfg> {
     __device__ bool setup(const Args &args, int b) {
         int k0;
         const int I = args.I;
-        if (!begin(args, b, 2 * I, k0)) return false;
+        if (!B::template begin<true>(args, b, 2 * I, k0)) return false;
         const int n0 = t.nt * C::BN, nw = min(C::BN, a.H - n0);
         const int64_t wo = (int64_t)n0 * I, so = (int64_t)n0 * (I / 32);
         const uint8_t *xs = x_scales(2 * I, k0);
@@ -353,12 +360,16 @@ struct FfnDX8 : Ffn8Base<Cfg> {
     }
 };
 
-// dy along H: a thread takes 8 values, 4 neighbouring lanes one 32-block.
-__global__ __launch_bounds__(256) void ffn_quantize_rows(const uint16_t *__restrict__ src, int64_t n8,
-                                                         uint8_t *__restrict__ el, uint8_t *__restrict__ sc) {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (c >= n8) return;   // whole groups of 4 lanes: rows are multiples of 128 values
-    const uint4 x = reinterpret_cast<const uint4 *>(src)[c];
+// dy along H: a thread takes 8 values, 4 neighbouring lanes one 32-block; a
+// workgroup 4 rows of 512 columns, whose blocks' rows lie side by side.
+constexpr int kQRows = 4, kQCols = 512;
+__global__ __launch_bounds__(64 * kQRows) void ffn_quantize_rows(const uint16_t *__restrict__ src, int T, int H,
+                                                                 uint8_t *__restrict__ el, uint8_t *__restrict__ sc) {
+    const uint32_t chunks = (uint32_t)(H + kQCols - 1) / kQCols;
+    const int t = (int)(blockIdx.x / chunks) * kQRows + (int)(threadIdx.x >> 6);
+    const int k = (int)(blockIdx.x % chunks) * kQCols + (int)(threadIdx.x & 63) * 8;
+    if (t >= T || k >= H) return;   // whole groups of 4 lanes: rows are multiples of 128 values
+    const uint4 x = *reinterpret_cast<const uint4 *>(src + (int64_t)t * H + k);
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     uint32_t amax = 0;
 #pragma unroll
@@ -367,8 +378,9 @@ __global__ __launch_bounds__(256) void ffn_quantize_rows(const uint16_t *__restr
     amax = max(amax, (uint32_t)__shfl_xor((int)amax, 2));
     const uint32_t sb = mx_scale_byte_bf16(amax);
     const int e = (int)sb - 127;
-    reinterpret_cast<uint2 *>(el)[c] = make_uint2(e4m3x4_bf16(w[0], w[1], e), e4m3x4_bf16(w[2], w[3], e));
-    if ((c & 3) == 0) sc[c >> 2] = (uint8_t)sb;
+    *reinterpret_cast<uint2 *>(el + tiled_at((uint32_t)T, (uint32_t)t, (uint32_t)k)) =
+        make_uint2(e4m3x4_bf16(w[0], w[1], e), e4m3x4_bf16(w[2], w[3], e));
+    if (k % 32 == 0) sc[((int64_t)t * H + k) / 32] = (uint8_t)sb;
 }
 
 template <class P>
@@ -487,9 +499,9 @@ hipError_t ffn_mx_backward(const FfnPlan &p, char *ws, const uint16_t *x, const 
     if (p.T > 0) {
         uint8_t *dyq = reinterpret_cast<uint8_t *>(ws + p.dy_q), *dyqs = reinterpret_cast<uint8_t *>(ws + p.dy_qs);
         {
-            const int64_t n8 = p.T * (int64_t)p.H / 8;
+            const unsigned grid = (unsigned)(ceil_div(p.T, kQRows) * ceil_div(p.H, kQCols));
             KernelTimer tm("ffn_quantize_rows", st);
-            ffn_quantize_rows<<<(unsigned)ceil_div(n8, 256), 256, 0, st>>>(dy, n8, dyq, dyqs);
+            ffn_quantize_rows<<<grid, 64 * kQRows, 0, st>>>(dy, a.T, p.H, dyq, dyqs);
         }
         a.x = dyq;
         a.xs = dyqs;
