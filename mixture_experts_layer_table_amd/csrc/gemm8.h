@@ -36,7 +36,8 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 template <class C>
 struct Fp8Stage {
     // waves 0-3 load the scales of 256 X rows (rows past a 128-row tile come as zeros), waves 4-7 those of W
-    static_assert((C::BM == 256 || C::BM == 128) && C::BN == 256 && C::NW == 8, "scale loads assume 8 waves, 256 W rows");
+    static_assert((C::BM == 256 || C::BM == 128) && C::BN == 256 && C::NW == 8,
+                  "scale loads assume 8 waves, 256 W rows");
     static constexpr int BYTES = C::STAGE_BYTES;
     static constexpr int NSCBUF = 3;                         // scale chunk buffers per operand (see ScaleLoader)
     static constexpr int SCBUF_BYTES = 256 * 16;             // one chunk: [256 rows][CB <= 16 bytes]
