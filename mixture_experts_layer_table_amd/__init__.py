@@ -753,8 +753,10 @@ def add_rmsnorm_backward(dy, sum, weight, rstd, dsum=None, p: float = 0.0, rng=N
     """Backward of add_rmsnorm() from its sum and rstd (mok_add_rmsnorm_backward).
     dy: bf16 [T, H]; dsum: [T, H] in sum's type, the gradient along the residual
     stream, or None. Returns a dict: dresidual [T, H] in sum's type, dx bf16
-    [T, H] (the same tensor as dresidual where both are bf16 and p == 0),
-    dweight fp32 [H]. ``workspace``: uint8, made here if None."""
+    [T, H], dweight fp32 [H]. ``grads``: the same keys, caller-given. Where both
+    are bf16 and p == 0, dx equals dresidual: it is the same tensor then, unless
+    ``grads`` holds a buffer of its own for it, which is written. ``workspace``:
+    uint8, made here if None."""
     shape, dev, dtype = sum.shape, sum.device, sum.dtype
     if len(shape) != 2:
         raise ValueError(f"sum: shape {tuple(shape)}, expected [T, H]")
@@ -771,8 +773,9 @@ def add_rmsnorm_backward(dy, sum, weight, rstd, dsum=None, p: float = 0.0, rng=N
     if grads is not None:
         _need(grads.get("dresidual"), "dresidual", dtype, shape, dev)
         _need(grads.get("dweight"), "dweight", _F32, (H,), dev)
-        if separate:
+        if separate or grads.get("dx") is not None:
             _need(grads.get("dx"), "dx", _BF16, shape, dev)
+            separate = separate or grads["dx"].data_ptr() != grads["dresidual"].data_ptr()
     if _elsewhere(dev):
         with torch.cuda.device(dev):
             return add_rmsnorm_backward(dy, sum, weight, rstd, dsum, p, rng, grads, workspace)
