@@ -308,7 +308,9 @@ mok_status mok_forward_noalloc(const mok_config *cfg, const mok_shape *shape,
  *                  [batch, K, rows] if 1 (quantizes the transpose)
  *   elems          device uint8 [batch, rows, K]
  *   scales         device uint8 [batch, rows, K/32]
- * K must be a multiple of 32. NaN/Inf inputs are unsupported.
+ * A run that holds a NaN or an infinity becomes NaN throughout (elements 0x7F or
+ * 0xFF); the same holds wherever the library quantizes rows itself.
+ * K must be a multiple of 32.
  */
 mok_status mok_mxfp8_quantize(const void *src, int64_t batch, int64_t rows, int64_t K,
                               int32_t src_is_k_by_rows, uint8_t *elems, uint8_t *scales,

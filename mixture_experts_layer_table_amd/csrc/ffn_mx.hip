@@ -378,8 +378,9 @@ __global__ __launch_bounds__(64 * kQRows) void ffn_quantize_rows(const uint16_t 
     amax = max(amax, (uint32_t)__shfl_xor((int)amax, 2));
     const uint32_t sb = mx_scale_byte_bf16(amax);
     const int e = (int)sb - 127;
+    const uint32_t nan = mx_nan_bf16(amax);
     *reinterpret_cast<uint2 *>(el + tiled_at((uint32_t)T, (uint32_t)t, (uint32_t)k)) =
-        make_uint2(e4m3x4_bf16(w[0], w[1], e), e4m3x4_bf16(w[2], w[3], e));
+        make_uint2(e4m3x4_bf16(w[0], w[1], e, nan), e4m3x4_bf16(w[2], w[3], e, nan));
     if (k % 32 == 0) sc[((int64_t)t * H + k) / 32] = (uint8_t)sb;
 }
 

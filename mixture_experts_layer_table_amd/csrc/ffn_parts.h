@@ -233,7 +233,7 @@ __device__ __forceinline__ uint32_t quantize_lane4(const float (&v)[4], uint32_t
     for (int off = 1; off <= 4; off <<= 1) amax = max(amax, (uint32_t)__shfl_xor((int)amax, off));
     scale = mx_scale_byte_f32(amax);
     const float q = mx_pow2_neg((int)scale - 127);
-    return e4m3x2_scaled(v[0] * q, v[1] * q) | (e4m3x2_scaled(v[2] * q, v[3] * q) << 16);
+    return mx_nan_f32(amax) | e4m3x2_scaled(v[0] * q, v[1] * q) | (e4m3x2_scaled(v[2] * q, v[3] * q) << 16);
 }
 
 // MXFP8 rows that the block quantizes itself (a, dy, dh) are K-tiled: blocks of 64

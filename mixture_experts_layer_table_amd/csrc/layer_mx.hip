@@ -80,9 +80,10 @@ struct GatherMx {
                 amax = max(amax, (uint32_t)__shfl_xor((int)amax, 2));
                 const uint32_t sb = mx_scale_byte_bf16(amax);
                 const int e = (int)sb - 127;
+                const uint32_t nan = mx_nan_bf16(amax);
                 uint32_t o[2];
 #pragma unroll
-                for (int d = 0; d < 2; ++d) o[d] = e4m3x4_bf16(w[2 * d], w[2 * d + 1], e);
+                for (int d = 0; d < 2; ++d) o[d] = e4m3x4_bf16(w[2 * d], w[2 * d + 1], e, nan);
                 if (c < n) {
                     *reinterpret_cast<uint2 *>(el + (int64_t)c * 8) = make_uint2(o[0], o[1]);
                     if ((c & 3) == 0) sc[c >> 2] = (uint8_t)sb;
@@ -578,9 +579,11 @@ __global__ __launch_bounds__(256) void quantize_cols(QuantCols q) {
         }
         const uint32_t sb = mx_scale_byte_bf16(amax);
         const int ex = (int)sb - 127;
+        const uint32_t nan = mx_nan_bf16(amax);
 #pragma unroll
         for (int d = 0; d < 8; ++d)
-            codes[c][b * 8 + d] = e4m3x4_bf16(x[4 * d] | (x[4 * d + 1] << 16), x[4 * d + 2] | (x[4 * d + 3] << 16), ex);
+            codes[c][b * 8 + d] = e4m3x4_bf16(x[4 * d] | (x[4 * d + 1] << 16), x[4 * d + 2] | (x[4 * d + 3] << 16), ex,
+                                              nan);
         if (col0 + c < q.ncols) q.sc[(int64_t)(col0 + c) * (q.Kp / 32) + p0 / 32 + b] = (uint8_t)sb;
     }
     __syncthreads();

@@ -29,9 +29,10 @@ __device__ __forceinline__ Enc16 encode_block16(const Block16 &b) {
     Enc16 r;
     r.scale = mx_scale_byte_f32(amax);
     const float sc = mx_pow2_neg((int)r.scale - 127);
+    const uint32_t nan = mx_nan_f32(amax);
 #pragma unroll
     for (int g4 = 0; g4 < 4; ++g4)
-        r.enc[g4] = e4m3x2_scaled(b.v[g4 * 4] * sc, b.v[g4 * 4 + 1] * sc) |
+        r.enc[g4] = nan | e4m3x2_scaled(b.v[g4 * 4] * sc, b.v[g4 * 4 + 1] * sc) |
                     (e4m3x2_scaled(b.v[g4 * 4 + 2] * sc, b.v[g4 * 4 + 3] * sc) << 16);
     return r;
 }

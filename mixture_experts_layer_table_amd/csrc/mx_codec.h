@@ -8,7 +8,10 @@
 //                -127, 127) + 127, which is max(0, biased exponent of amax - 8)
 //                (subnormal maxima land on the lower clamp)
 //   element    = the value times 2^-e rounded to E4M3's quantum for its binade,
-//                to nearest even, saturated to 448 (0x7E), sign kept.
+//                to nearest even, saturated to 448 (0x7E), sign kept
+// A block that holds a NaN or an infinity has no such scale: all its elements
+// become NaN, as an E8M0 NaN would make them, so that the products of its row
+// show it instead of carrying on with finite numbers.
 #pragma once
 #include "common.h"
 
@@ -25,6 +28,17 @@ __device__ __forceinline__ uint32_t mx_scale_byte_f32(uint32_t amax_bits /* |fp3
     return mx_scale_from_exp(amax_bits >> 23, amax_bits == 0);
 }
 
+// What to OR onto four codes of a block: nothing, or E4M3FN's NaN (the low
+// seven bits of each byte, either sign) where its largest magnitude is no finite
+// number. The bits of a NaN lie above infinity's, so one comparison a block finds
+// both; per element the clamp below would have to tell a NaN from a number.
+__device__ __forceinline__ uint32_t mx_nan_bf16(uint32_t amax_bits) {
+    return amax_bits >= 0x7F80u ? 0x7F7F7F7Fu : 0u;
+}
+__device__ __forceinline__ uint32_t mx_nan_f32(uint32_t amax_bits) {
+    return amax_bits >= 0x7F800000u ? 0x7F7F7F7Fu : 0u;
+}
+
 // E4M3FN code of a finite value v times 2^-e. 2^-e is a normal float for
 // every scale exponent a block can have (e = scale byte - 127, -127 .. 119),
 // so v * 2^-e is exact wherever E4M3 can represent anything (below 2^-126 it
@@ -39,7 +53,7 @@ __device__ __forceinline__ uint32_t mx_scale_byte_f32(uint32_t amax_bits /* |fp3
 __device__ __forceinline__ float mx_pow2_neg(int e) { return __uint_as_float((uint32_t)(127 - e) << 23); }
 __device__ __forceinline__ float mx_clamp448(float v) { return fminf(fmaxf(v, -448.0f), 448.0f); }
 
-// Two codes (bytes 0 and 1) of a and b, already multiplied by 2^-e.
+// Two codes (bytes 0 and 1) of finite a and b, already multiplied by 2^-e.
 __device__ __forceinline__ uint32_t e4m3x2_scaled(float a, float b) {
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(mx_clamp448(a), mx_clamp448(b), 0, false) & 0xFFFFu;
 }
@@ -50,10 +64,11 @@ __device__ __forceinline__ uint32_t e4m3_encode_f32(uint32_t b, int e) {
 __device__ __forceinline__ uint32_t e4m3_encode_bf16(uint32_t b, int e) {
     return e4m3_encode_f32(b << 16, e);
 }
-// Four codes (bytes 0..3) of the bf16 pairs w0 = (lo, hi) and w1 = (lo, hi).
-__device__ __forceinline__ uint32_t e4m3x4_bf16(uint32_t w0, uint32_t w1, int e) {
+// Four codes (bytes 0..3) of the bf16 pairs w0 = (lo, hi) and w1 = (lo, hi);
+// nan: the block's mx_nan_bf16.
+__device__ __forceinline__ uint32_t e4m3x4_bf16(uint32_t w0, uint32_t w1, int e, uint32_t nan) {
     const float s = mx_pow2_neg(e);
-    return e4m3x2_scaled(__uint_as_float(w0 << 16) * s, __uint_as_float(w0 & 0xFFFF0000u) * s) |
+    return nan | e4m3x2_scaled(__uint_as_float(w0 << 16) * s, __uint_as_float(w0 & 0xFFFF0000u) * s) |
            (e4m3x2_scaled(__uint_as_float(w1 << 16) * s, __uint_as_float(w1 & 0xFFFF0000u) * s) << 16);
 }
 

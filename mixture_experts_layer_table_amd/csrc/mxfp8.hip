@@ -51,10 +51,11 @@ __global__ __launch_bounds__(256) void mxfp8_quantize_kernel(const uint16_t *__r
     for (int i = 0; i < 32; ++i) amax = max(amax, v[i] & 0x7FFFu);   // |bf16| orders like its bits
     const uint32_t sb = mx_scale_byte_bf16(amax);
     const int e = (int)sb - 127;
+    const uint32_t nan = mx_nan_bf16(amax);
     uint32_t packed[8];
 #pragma unroll
     for (int w = 0; w < 8; ++w) {
-        packed[w] = e4m3x4_bf16(v[w * 4] | (v[w * 4 + 1] << 16), v[w * 4 + 2] | (v[w * 4 + 3] << 16), e);
+        packed[w] = e4m3x4_bf16(v[w * 4] | (v[w * 4 + 1] << 16), v[w * 4 + 2] | (v[w * 4 + 3] << 16), e, nan);
     }
     uint4 *dst = reinterpret_cast<uint4 *>(elems + (b * rows + r) * K + kb * 32);
     dst[0] = make_uint4(packed[0], packed[1], packed[2], packed[3]);

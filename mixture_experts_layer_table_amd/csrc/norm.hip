@@ -127,9 +127,10 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_forward(NormFwdArgs a) {
             amax = max(amax, (uint32_t)__shfl_xor((int)amax, 1));   // the 4 lanes of a 32-block
             amax = max(amax, (uint32_t)__shfl_xor((int)amax, 2));
             const uint32_t sb = mx_scale_byte_f32(amax);
+            const uint32_t nan = mx_nan_f32(amax);
             const float q = mx_pow2_neg((int)sb - 127);
             auto codes = [&](int j) {
-                return e4m3x2_scaled(v[i][j] * q, v[i][j + 1] * q) |
+                return nan | e4m3x2_scaled(v[i][j] * q, v[i][j + 1] * q) |
                        (e4m3x2_scaled(v[i][j + 2] * q, v[i][j + 3] * q) << 16);
             };
             if (ok) {
