@@ -59,12 +59,13 @@ struct NormFwdArgs {
     DropArgs drop;
     float eps, inv_h;
     int H;
+    int64_t row0;   // first row of the launch
 };
 
 template <Elem RES, Elem SUM, int CH>
 __global__ __launch_bounds__(64 * kMaxWaves) void norm_forward(NormFwdArgs a) {
     __shared__ float red[kMaxWaves];
-    const int64_t row = blockIdx.x;
+    const int64_t row = a.row0 + blockIdx.x;
     const int nc = a.H / 8, nt = (int)blockDim.x, tid = (int)threadIdx.x;
     const int64_t base = row * nc;   // in chunks
     Raw8<kBf16> xr[CH], wr[CH];
@@ -306,20 +307,27 @@ int64_t norm_backward_shares(int64_t T, int H) {
     return std::min<int64_t>(T, 2 * std::max(backward_target(H, 1), backward_target(H, 1 << 20)));
 }
 
+// Threads of one forward launch: a grid takes fewer than 2^32, so rows past that
+// many waves (2^25 rows at the narrowest) go to further launches.
+constexpr int64_t kLaunchThreads = int64_t(1) << 31;
+
 mok_status launch_add_rmsnorm(const NormCall &c, hipStream_t st) {
-    const NormFwdArgs a{c.x,  c.residual, c.weight, c.sum, c.y, c.elems, c.scales, c.rstd, drop_args(c.p, c.rng),
-                        c.eps, 1.0f / (float)c.H, c.H};
+    NormFwdArgs a{c.x,  c.residual, c.weight, c.sum, c.y, c.elems, c.scales, c.rstd, drop_args(c.p, c.rng),
+                        c.eps, 1.0f / (float)c.H, c.H, 0};
     const RowShape rs = row_shape(c.H, c.T);
-    KernelTimer tm("add_rmsnorm", st);
+    const int64_t rows = kLaunchThreads / (64 * rs.waves);
     with_ch(rs.ch, [&](auto ch) {
         constexpr int CH = decltype(ch)::value;
-        const dim3 g((unsigned)c.T), b(64 * rs.waves);
-        if (c.f32_stream) {
-            if (c.residual) norm_forward<kF32, kF32, CH><<<g, b, 0, st>>>(a);
-            else norm_forward<kNone, kF32, CH><<<g, b, 0, st>>>(a);
-        } else {
-            if (c.residual) norm_forward<kBf16, kBf16, CH><<<g, b, 0, st>>>(a);
-            else norm_forward<kNone, kBf16, CH><<<g, b, 0, st>>>(a);
+        for (; a.row0 < c.T; a.row0 += rows) {
+            const dim3 g((unsigned)std::min(rows, c.T - a.row0)), b(64 * rs.waves);
+            KernelTimer tm("add_rmsnorm", st);
+            if (c.f32_stream) {
+                if (c.residual) norm_forward<kF32, kF32, CH><<<g, b, 0, st>>>(a);
+                else norm_forward<kNone, kF32, CH><<<g, b, 0, st>>>(a);
+            } else {
+                if (c.residual) norm_forward<kBf16, kBf16, CH><<<g, b, 0, st>>>(a);
+                else norm_forward<kNone, kBf16, CH><<<g, b, 0, st>>>(a);
+            }
         }
     });
     return check_hip(hipGetLastError(), "mok_add_rmsnorm");
