@@ -376,7 +376,7 @@ mok_status mok_route_backward(const int32_t *topk_ids, const float *topk_w, cons
 
 /*
  * out = residual + dropout(x).
- *   x         device bf16 [n], any n in [0, 2^40)
+ *   x         device bf16 [n], any n in [0, 2^37 - 8192]
  *   residual  device stream_dtype [n], or NULL (then out = dropout(x))
  *   p         drop probability in [0, 1)
  *   out       device stream_dtype [n]; may be residual's buffer, or x's when

@@ -15,8 +15,6 @@ bool aligned4(const void *p) { return p != nullptr && (reinterpret_cast<uintptr_
 bool dev_ok(const void *p) { return p != nullptr && aligned16(p); }
 bool dev_ok_or_null(const void *p) { return aligned16(p); }
 
-constexpr int64_t kMaxDropout = int64_t(1) << 40;   // elements of one dropout call
-
 bool stream_ok(int32_t dtype) { return dtype == MOK_STREAM_BF16 || dtype == MOK_STREAM_F32; }
 // p in [0, 1); the state is read only where something can be dropped
 bool drop_ok(float p, const uint64_t *rng) {
@@ -226,7 +224,7 @@ mok_status mok_route_backward(const int32_t *topk_ids, const float *topk_w, cons
 
 mok_status mok_dropout(const void *x, const void *residual, int64_t n, float p, const uint64_t *rng,
                        int32_t stream_dtype, void *out, void *stream) {
-    if (n < 0 || n >= kMaxDropout || !stream_ok(stream_dtype) || !drop_ok(p, rng)) return MOK_ERROR_INVALID_VALUE;
+    if (n < 0 || n > kMaxDropout || !stream_ok(stream_dtype) || !drop_ok(p, rng)) return MOK_ERROR_INVALID_VALUE;
     if (n == 0) return MOK_OK;
     if (!dev_ok(x) || !dev_ok_or_null(residual) || !dev_ok(out)) return MOK_ERROR_INVALID_VALUE;
     const bool f32 = stream_dtype == MOK_STREAM_F32;
@@ -241,7 +239,7 @@ mok_status mok_dropout(const void *x, const void *residual, int64_t n, float p, 
 
 mok_status mok_dropout_backward(const void *dy, int64_t n, float p, const uint64_t *rng, int32_t stream_dtype,
                                 void *dx, void *stream) {
-    if (n < 0 || n >= kMaxDropout || !stream_ok(stream_dtype) || !drop_ok(p, rng)) return MOK_ERROR_INVALID_VALUE;
+    if (n < 0 || n > kMaxDropout || !stream_ok(stream_dtype) || !drop_ok(p, rng)) return MOK_ERROR_INVALID_VALUE;
     if (n == 0) return MOK_OK;
     if (!dev_ok(dy) || !dev_ok(dx)) return MOK_ERROR_INVALID_VALUE;
     const bool f32 = stream_dtype == MOK_STREAM_F32;

@@ -18,6 +18,8 @@ namespace {
 
 constexpr int kDropThreads = 256;
 constexpr int kDropChunks = 4;   // chunks in flight per thread
+static_assert((kMaxDropout + 8191) / 8192 * kDropThreads < int64_t(1) << 32 && kDropThreads * kDropChunks * 8 == 8192,
+              "the largest call fits one grid");
 
 template <Elem IN, Elem RES, Elem OUT>
 __global__ __launch_bounds__(kDropThreads) void dropout_kernel(const void *x, const void *residual,

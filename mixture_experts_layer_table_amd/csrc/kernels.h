@@ -35,6 +35,9 @@ mok_status launch_route(const float *logits, int64_t T, int E, int k, int32_t *i
 mok_status launch_route_backward(const int32_t *ids, const float *w, const float *dw, int64_t T, int E, int k,
                                  float *dl, hipStream_t st);
 
+// Most elements of one dropout call: a grid takes fewer than 2^32 threads, and a
+// workgroup of 256 takes 8,192 elements.
+constexpr int64_t kMaxDropout = ((int64_t(1) << 24) - 1) * 8192;
 mok_status launch_dropout(const uint16_t *x, const void *residual, int64_t n, float p, const uint64_t *rng,
                           bool f32_stream, void *out, hipStream_t st);
 
