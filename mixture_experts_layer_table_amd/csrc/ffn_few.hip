@@ -256,9 +256,6 @@ __global__ __launch_bounds__(kThreads, 2) void few_down(FewArgs a, int rows) {
 
 // ----------------------------------------------------------------------------- MXFP8
 
-// 2^(e - 127) for a scale byte e (0 is the subnormal 2^-127).
-__device__ __forceinline__ float scale_value(uint32_t e) { return __uint_as_float(e ? e << 23 : 0x00400000u); }
-
 // The values of 4 E4M3 codes.
 __device__ __forceinline__ f32x4_t unpack_fp8x4(uint32_t w) {
     const f32x2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
@@ -361,10 +358,11 @@ constexpr int kRowsPerGroup = 4;   // output columns (weight rows) per group of 
 
 template <int T>
 __global__ __launch_bounds__(kThreads, 2) void few_down8(Few8Args a, int rows) {
-    extern __shared__ __attribute__((aligned(16))) float few_lds[];   // the values that a's codes hold, [T][I]
+    extern __shared__ __attribute__((aligned(16))) float few_lds[];   // what a's codes hold, without their scales: [T][I]
     const int I = a.I, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, per = 64 / a.lanes, l = lane % a.lanes;
     const int n0 = (((int)blockIdx.x * kWaves + wave) * per + lane / a.lanes) * kRowsPerGroup;
     const int n = (I + 16 * a.lanes - 1) / (16 * a.lanes);
+    uint32_t *as = reinterpret_cast<uint32_t *>(few_lds + T * I);   // a's scale bytes, [T][I / 32]
     float acc[T][kRowsPerGroup];
 #pragma unroll
     for (int t = 0; t < T; ++t)
@@ -396,7 +394,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_down8(Few8Args a, int rows) {
                 const float v[4] = {p[0], p[1], p[2], p[3]};
                 uint32_t sc;
                 const uint32_t code = quantize_lane4(v, sc);
-                *reinterpret_cast<f32x4_t *>(few_lds + e) = unpack_fp8x4(code) * scale_value(sc);
+                *reinterpret_cast<f32x4_t *>(few_lds + e) = unpack_fp8x4(code);
+                if (e % 32 == 0) as[e / 32] = sc;
             }
             __syncthreads();
         }
@@ -405,7 +404,6 @@ __global__ __launch_bounds__(kThreads, 2) void few_down8(Few8Args a, int rows) {
             for (int r = 0; r < kRowsPerGroup; ++r) {
                 float f[16];
                 unpack_fp8x16(wv[r], f);
-                const float q = scale_value(we[r]);
 #pragma unroll
                 for (int t = 0; t < T; ++t) {
                     float d = 0.0f;
@@ -415,7 +413,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_down8(Few8Args a, int rows) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) d = __builtin_fmaf(f[j4 * 4 + j], av[j], d);
                     }
-                    acc[t][r] = __builtin_fmaf(d, q, acc[t][r]);
+                    // half of one 32-block, its two scales as one exponent (as in gate/up)
+                    acc[t][r] += __builtin_ldexpf(d, (int)(we[r] + as[t * (I / 32) + k / 32]) - 254);
                 }
             }
         }
@@ -483,7 +482,7 @@ hipError_t ffn_few_mx_forward(const FfnPlan &p, char *ws, const uint8_t *x_elems
         a.lanes = lanes_for(p.I);
         KernelTimer tm("ffn_few_down_mx", st);
         const unsigned grid = (unsigned)ceil_div(p.H, kWaves * (64 / a.lanes) * kRowsPerGroup);
-        few_down8<T><<<grid, kThreads, sizeof(float) * T * p.I, st>>>(a, rows);
+        few_down8<T><<<grid, kThreads, sizeof(float) * T * (p.I + p.I / 32), st>>>(a, rows);
     });
     return hipGetLastError();
 }

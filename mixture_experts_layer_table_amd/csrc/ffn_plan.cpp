@@ -66,8 +66,9 @@ FfnSplit choose(int64_t T, int64_t N, int64_t n_tiles, int steps, bool mx) {
 // 1,024 x 512 12 against 16 and 7 against 15); two rows in MXFP8 (20 against 24,
 // 10 against 15) and in BF16 up to 2^23 weights a matrix (4,096 x 1,024 19 us
 // against 24; 7,168 x 2,048 32 against 29). Its buffers in LDS stay under
-// 64 KiB (the rows of a in fp32), and BF16 cuts the gate/up product into at
-// most 16 runs of at most 2,048 rows, about one workgroup per compute unit.
+// 64 KiB (the rows of a in fp32, in MXFP8 with a scale for each 32 values), and
+// BF16 cuts the gate/up product into at most 16 runs of at most 2,048 rows,
+// about one workgroup per compute unit.
 void plan_few(FfnPlan &p) {
     p.few_runs = p.few_run_rows = 0;
     if (p.T < 1 || p.T > kFewRows || p.T * p.I > 15 * 1024 || p.H > 16 * 2048) return;
