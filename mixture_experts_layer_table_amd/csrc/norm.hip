@@ -57,7 +57,7 @@ struct NormFwdArgs {
     uint8_t *elems, *scales;
     float *rstd;
     DropArgs drop;
-    float eps, inv_h;
+    float eps;
     int H;
     int64_t row0;   // first row of the launch
 };
@@ -110,7 +110,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_forward(NormFwdArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(v[i][j], v[i][j], ss);
     }
-    const float r = 1.0f / sqrtf(__builtin_fmaf(block_sum(ss, red), a.inv_h, a.eps));
+    // a division: 1 / H as a factor would carry its own rounding into every row
+    const float r = 1.0f / sqrtf(block_sum(ss, red) / (float)a.H + a.eps);
     if (tid == 0) a.rstd[row] = r;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -151,7 +152,6 @@ struct NormBwdArgs {
     uint16_t *dx;
     float *part;   // [workgroups][H]: each workgroup's share of dweight
     DropArgs drop;
-    float inv_h;
     int H;
     int64_t T;
 };
@@ -204,7 +204,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void norm_backward(NormBwdArgs a) {
                 }
             }
         }
-        const float cr = block_sum(dot, red[turn]) * a.inv_h * r * r;
+        const float cr = block_sum(dot, red[turn]) / (float)a.H * r * r;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int c = i * nt + tid;
@@ -313,7 +313,7 @@ constexpr int64_t kLaunchThreads = int64_t(1) << 31;
 
 mok_status launch_add_rmsnorm(const NormCall &c, hipStream_t st) {
     NormFwdArgs a{c.x,  c.residual, c.weight, c.sum, c.y, c.elems, c.scales, c.rstd, drop_args(c.p, c.rng),
-                        c.eps, 1.0f / (float)c.H, c.H, 0};
+                        c.eps, c.H, 0};
     const RowShape rs = row_shape(c.H, c.T);
     const int64_t rows = kLaunchThreads / (64 * rs.waves);
     with_ch(rs.ch, [&](auto ch) {
@@ -335,7 +335,7 @@ mok_status launch_add_rmsnorm(const NormCall &c, hipStream_t st) {
 
 mok_status launch_add_rmsnorm_backward(const NormBackwardCall &c, hipStream_t st) {
     const NormBwdArgs a{c.dy,  c.sum, c.dsum, c.weight, c.rstd, c.dres, c.dx, c.part, drop_args(c.p, c.rng),
-                        1.0f / (float)c.H, c.H, c.T};
+                        c.H, c.T};
     const int blocks = norm_backward_blocks(c.T, c.H);
     const RowShape rs = row_shape(c.H, c.T);
     if (blocks > 0) {

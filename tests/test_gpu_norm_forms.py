@@ -43,3 +43,18 @@ def test_the_returned_gradients_serve_as_buffers():
     assert again["dx"].data_ptr() == again["dresidual"].data_ptr()
     for n in want:
         assert torch.equal(again[n], want[n]), n
+
+
+@pytest.mark.parametrize("width", [56, 512, 1000, 7168])
+@pytest.mark.parametrize("value", [1.5, 1.75, 7.0])
+def test_rows_of_one_value_have_its_exact_norm(width, value):
+    # every partial sum of the squares is exact (a multiple of 2^-4 below 2^20), so their mean is value^2 and 1 / rms is
+    # 1 / value rounded once
+    x = torch.full((3, width), value, dtype=torch.bfloat16, device=DEV)
+    one = torch.ones(width, dtype=torch.bfloat16, device=DEV)
+    r = mok.add_rmsnorm(x, one, 0.0)
+    assert torch.equal(r["rstd"].cpu(), torch.full((3,), value).reciprocal())
+    # the gradient of a constant row through the norm is dy - mean(dy) times that: dy = 1 leaves only the roundings of
+    # rstd (twice), of two products with it and of the one with sum, at most 5 * 2^-24 of 1 / value
+    g = mok.add_rmsnorm_backward(torch.ones_like(x), r["sum"], one, r["rstd"])
+    assert (g["dx"].abs() <= 2.0 ** -21 / value).all()
