@@ -420,15 +420,10 @@ hipError_t backward_bf16(const FfnPlan &p, char *ws, const uint16_t *x, const mo
     a.len = p.dx.len;
     const FfnWgradArgs gu{a.T, p.H, 2 * p.I, p.I, p.I, x, a.dh, dw_gate, dw_up};
     const FfnWgradArgs wd{a.T, p.I, p.H, p.H, p.H, a.a, dy, dw_down, nullptr};
-    if (p.dx.bm == CfgS::BM && p.wgrad_bm == CfgS::BM) {
-        // with more tiles than compute units, two workgroups a unit (1,001 and
-        // 2,048 rows of 4,096 x 1,024: backward 84 -> 78 and 142 -> 131 us);
-        // with fewer, the deeper ring (2,048 rows of 1,024 x 512: 60 us against 71)
-        const int64_t tiles = wgrad_grid(gu.M, gu.N, CfgS::BM) + wgrad_grid(wd.M, wd.N, CfgS::BM) +
-                              ffn_grid(p.T, CfgS::BM, a.n_tiles, a.splits);
-        e = tiles > 256 ? launch_grads<CfgW, CfgW>(gu, wd, a, st) : launch_grads<CfgS, CfgS>(gu, wd, a, st);
-    } else if (p.dx.bm == CfgS::BM)
-        e = launch_grads<CfgS, CfgA>(gu, wd, a, st);
+    if (p.grads_two)
+        e = launch_grads<CfgW, CfgW>(gu, wd, a, st);
+    else if (p.dx.bm == CfgS::BM)
+        e = p.wgrad_bm == CfgS::BM ? launch_grads<CfgS, CfgS>(gu, wd, a, st) : launch_grads<CfgS, CfgA>(gu, wd, a, st);
     else
         e = p.wgrad_bm == CfgS::BM ? launch_grads<CfgA, CfgS>(gu, wd, a, st) : launch_grads<CfgA, CfgA>(gu, wd, a, st);
     if (e == hipSuccess && p.T > 0 && p.dx.splits > 1) {

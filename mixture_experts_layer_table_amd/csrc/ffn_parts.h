@@ -15,6 +15,8 @@
 namespace mok {
 namespace {
 
+static_assert(kXcds == kGridStep, "the plan counts workgroups as the launches do");
+
 // ----------------------------------------------------------------------------- tiles
 
 struct FfnTile {

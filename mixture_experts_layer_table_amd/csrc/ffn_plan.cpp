@@ -25,6 +25,9 @@ struct Carver {
     }
 };
 
+// Workgroups of a product of n tiles (ffn_grid, wgrad_grid).
+int64_t grid(int64_t n) { return ceil_div(n, kGridStep) * kGridStep; }
+
 size_t part_bytes(int64_t T, int H, int I) {
     const int64_t widest = std::max<int64_t>(H, 2 * (int64_t)I);
     return (size_t)std::min<int64_t>((int64_t)kPartBytes, (int64_t)kMaxSplits * T * widest * 4);
@@ -113,6 +116,15 @@ mok_status make_ffn_plan(int64_t T, int32_t H, int32_t I, int32_t precision, Ffn
     p.dx = choose(T, H, ceil_div(H, kTileN), 2 * I / k, mx);
     const int64_t big = ceil_div(2 * (int64_t)I, 256) * ceil_div(H, 256) + ceil_div(H, 256) * ceil_div(I, 256);
     p.wgrad_bm = big < kUnits ? 128 : 256;
+    // dx and the weight gradients in one launch, on 128 rows both: with more tiles
+    // than compute units, two workgroups a unit (1,001 and 2,048 rows of
+    // 4,096 x 1,024: backward 84 -> 78 and 142 -> 131 us); with fewer, the deeper
+    // ring (2,048 rows of 1,024 x 512: 60 us against 71)
+    p.grads_two = !mx && p.dx.bm == 128 && p.wgrad_bm == 128 &&
+                  grid(ceil_div(H, 128) * ceil_div(2 * (int64_t)I, kTileN)) +
+                          grid(ceil_div(I, 128) * ceil_div(H, kTileN)) +
+                          grid(ceil_div(T, 128) * ceil_div(H, kTileN) * p.dx.splits) >
+                      kUnits;
     Carver w;
     p.part = w.take(part_bytes(T, H, I));
     p.a = w.take((size_t)T * I * 2);

@@ -16,6 +16,9 @@ struct FfnSplit {
     int bm, splits, len;
 };
 
+// Workgroups of a product come in multiples of the dies (kXcds on the device side).
+constexpr int kGridStep = 8;
+
 // Most rows that take the few-rows kernels (ffn_few.hip).
 constexpr int kFewRows = 2;
 
@@ -24,7 +27,8 @@ struct FfnPlan {
     int H, I;
     bool mx;
     FfnSplit gate_up, down, da, dx;
-    int wgrad_bm;   // m-tile rows of the weight gradients
+    int wgrad_bm;     // m-tile rows of the weight gradients
+    bool grads_two;   // BF16, dx and the weight gradients on 128 rows: two workgroups a unit
     // few-rows forward: 0 runs where the tile kernels are taken instead;
     // BF16 gate/up: runs of few_run_rows rows of the weights
     int few_runs, few_run_rows;
