@@ -47,9 +47,9 @@ __device__ __forceinline__ uint4 load_once(const void *p) {
     return make_uint4(v.x, v.y, v.z, v.w);
 }
 
-// 16 bytes at byte voff + soff (soff uniform, itself inside the range: the check
-// compares voff with what soff leaves of it) of a range; past it: zeros, with no
-// branch. Cached: two workgroups share each line of W_down (non-temporal, the
+// 16 bytes at byte voff + soff (soff uniform) of a range; past it: zeros, with
+// no branch (gfx950 checks the sum of both offsets, also where soff alone lies past
+// the range: held on a buffer whose memory goes on behind the range). Cached: two workgroups share each line of W_down (non-temporal, the
 // down kernel took 12.3 us instead of 10.7 at 7,168 x 2,048).
 __device__ __forceinline__ uint4 load16(brsrc_t r, uint32_t voff, uint32_t soff) {
     typedef uint32_t v4u __attribute__((ext_vector_type(4)));
@@ -99,10 +99,9 @@ __global__ __launch_bounds__(kThreads, 2) void few_gate_up(FewArgs a, int rows) 
     for (int b = 0; b < n; b += kBatch) {
         uint4 gv[kBatch], uv[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {   // past the run: its last rows again, left out below
-            const uint32_t s = (uint32_t)min(b + i, n - 1) * step;
-            gv[i] = load16(g, v0, s);
-            uv[i] = load16(u, v0, s);
+        for (int i = 0; i < kBatch; ++i) {   // rows past the run: zeros
+            gv[i] = load16(g, v0, (uint32_t)(b + i) * step);
+            uv[i] = load16(u, v0, (uint32_t)(b + i) * step);
         }
         if (b == 0) {
             if (e0 < T * kn) put_x4(e0, x0);
@@ -214,8 +213,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_down(FewArgs a, int rows) {
     for (int b = 0; b < n; b += kBatch) {
         uint4 wv[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)   // rows past I: zeros; past the last 128: those again, left out below
-            wv[i] = load16(w, v0, (uint32_t)min(b + i, n - 1) * step);
+        for (int i = 0; i < kBatch; ++i) wv[i] = load16(w, v0, (uint32_t)(b + i) * step);   // rows past I: zeros
         if (b == 0) {
             for (int e = e0; e < T * I; e += kThreads * 4) {
                 if (e != e0) load_runs(a, rows, e, hg, hu);

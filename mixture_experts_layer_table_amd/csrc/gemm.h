@@ -229,7 +229,7 @@ struct RowLoader {
     __device__ void issue(int k0, uint32_t tile) const {
         const bool second = k0 >= ksplit;
         const rsrc_t r = second ? res2 : res;
-        if (kblock) {   // the whole offset in voffset: the range check leaves soffset out
+        if (kblock) {   // the whole offset in voffset; the range check counts both offsets, as it must below
             const uint32_t kb = (uint32_t)(k0 >> 5) * kblock;
 #pragma unroll
             for (int i = 0; i < IPW; ++i) load_lds16(res, voff + kb + (uint32_t)(i * 1024), 0, tile + lds0 + i * 1024);
