@@ -49,8 +49,9 @@ __device__ __forceinline__ uint4 load_once(const void *p) {
 
 // 16 bytes at byte voff + soff (soff uniform) of a range; past it: zeros, with
 // no branch (gfx950 checks the sum of both offsets, also where soff alone lies past
-// the range: held on a buffer whose memory goes on behind the range). Cached: two workgroups share each line of W_down (non-temporal, the
-// down kernel took 12.3 us instead of 10.7 at 7,168 x 2,048).
+// the range: held on a buffer whose memory goes on behind the range). Cached: two
+// workgroups share each line of W_down (non-temporal, the down kernel took 12.3 us
+// instead of 10.7 at 7,168 x 2,048).
 __device__ __forceinline__ uint4 load16(brsrc_t r, uint32_t voff, uint32_t soff) {
     typedef uint32_t v4u __attribute__((ext_vector_type(4)));
     const v4u v = __builtin_amdgcn_raw_buffer_load_b128(r, (int)voff, (int)soff, 0);

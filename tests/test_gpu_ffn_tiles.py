@@ -99,3 +99,42 @@ def test_mxfp8(T, H, I, addend):
     rows["dx"] = rel_rows(g["dx"], r["dx"])
     assert all(v < TOL_MX for v in errs.values()), errs
     assert all(v < 4 * TOL_MX for v in rows.values()), rows
+
+
+@pytest.mark.parametrize("H,I", [(128, 1 << 20), (1 << 20, 128)])
+def test_mxfp8_widest_rows(H, I):
+    # the widest rows, as test_gpu_ffn.py has them in BF16: contraction axes of 2^20 and 2^21 values, K-tiled
+    print(f"[ffn tiles] mxfp8 widest H={H} I={I}", flush=True)
+    c = Case(3, H, I, True, 72)
+    o = operands(c)
+    out, h = c.forward()
+    ref, rh, _ = R.forward(**o, addend=c.add.double(), fq=R.fake_quant)
+    errs = dict(out=rel(out, ref), h=rel(h, rh))
+    g = c.backward(h)
+    r = R.backward(**o, h=h.double(), dy=c.dy.double(), addend=c.add.double(), fq=R.fake_quant)
+    errs.update({n: rel(g[n], r[n]) for n in g})
+    assert all(v < TOL_MX for v in errs.values()), errs
+
+
+def test_mxfp8_longest_batch():
+    # T * I * 4 one row short of 2 GiB at the narrowest width: the K-tiled rows' last offsets
+    T, H, I = (1 << 22) - 1, 128, 128
+    print(f"[ffn tiles] mxfp8 longest T={T}", flush=True)
+    c = Case(T, H, I, True, 82)
+    out, h = c.forward()
+    g = c.backward(h)
+    w = dict(wg=c.wg.double(), wu=c.wu.double(), wd=c.wd.double())
+    dw = {n: 0.0 for n in ("dw_gate", "dw_up", "dw_down")}
+    for a in range(0, T, 1 << 19):
+        s = slice(a, min(a + (1 << 19), T))
+        x, dy, add, hs = (t[s].double() for t in (c.x, c.dy, c.add, h))
+        ref, rh, _ = R.forward(x, **w, addend=add, fq=R.fake_quant)
+        r = R.backward(x, **w, h=hs, dy=dy, addend=add, fq=R.fake_quant)
+        for n, got, want in (("out", out[s], ref), ("h", h[s], rh), ("dx", g["dx"][s], r["dx"])):
+            # the worst of four million rows: a tie taken the other way moves one of its 128 operands by at most 2^-3 of
+            # itself, and one of 4 times their rms is 4 / sqrt(128) of the row: 0.044, twice that for two
+            assert rel(got, want) < TOL_MX and rel_rows(got, want) < 8 * TOL_MX, (n, a)
+        for n in dw:
+            dw[n] = dw[n] + r[n]
+    for n in dw:
+        assert rel(g[n], dw[n]) < TOL_MX, n
