@@ -458,6 +458,11 @@ mok_status mok_add_rmsnorm_backward(const mok_norm_shape *shape, void *workspace
  * precision is MOK_BF16 or MOK_MXFP8 (weight gradients in BF16).
  * Weights are a mok_weights for one expert (E = 1), in the orientations that
  * struct describes.
+ * Between the products, a = silu(x W_gate) * (x W_up) and dh are operands of
+ * fewer bits than their fp32 sums: in MOK_BF16 both are rounded to bf16 once (the
+ * forward of one row, and of two at the smaller sizes, keeps a in fp32); in
+ * MOK_MXFP8 both, and dy, are quantized from fp32 (dy from bf16) for the products
+ * with a weight and rounded to bf16 for the weight gradients.
  */
 typedef struct mok_ffn_shape {
     int64_t T;

@@ -860,7 +860,8 @@ def ffn_forward(ws: FfnWorkspace, x, weights: mok_weights, addend=None, out=None
     """Dense gated feed-forward block (mok_ffn_forward): out = addend +
     (silu(x W_gate) * (x W_up)) W_down. x: bf16 [T, H] (T up to ws.T), or in
     MXFP8 the pair (elems uint8 [T, H], scales uint8 [T, H/32]) that
-    add_rmsnorm(mxfp8=True) or mxfp8_quantize gives. addend: bf16 [T, H] or None;
+    add_rmsnorm(mxfp8=True) gives, or mxfp8_quantize of x[None] without its
+    leading dimension. addend: bf16 [T, H] or None;
     ``out`` may be addend. Returns (out bf16 [T, H], h bf16 [T, 2I] for the
     backward, or None with save_h=False and no ``h``)."""
     buf, H, I = ws.buffer, ws.H, ws.I

@@ -66,7 +66,7 @@ FfnSplit choose(int64_t T, int64_t N, int64_t n_tiles, int steps, bool mx) {
 
 // The few-rows forward, where it is faster than the tiles (GPU time of a call):
 // one row always (7,168 x 2,048 BF16 24 us against 28, MXFP8 16 against 24;
-// 1,024 x 512 12 against 16 and 7 against 15); two rows in MXFP8 (20 against 24,
+// 1,024 x 512 12 against 16 and 7 against 15); two rows in MXFP8 (21 against 24,
 // 10 against 15) and in BF16 up to 2^23 weights a matrix (4,096 x 1,024 19 us
 // against 24; 7,168 x 2,048 32 against 29). Its buffers in LDS stay under
 // 64 KiB (the rows of a in fp32, in MXFP8 with a scale for each 32 values), and

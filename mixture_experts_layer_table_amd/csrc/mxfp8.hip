@@ -2,7 +2,7 @@
 // Key-concepts table: weights are quantized before the kernel runs), in the
 // OCP MX v1.0 MXFP8 block format: 32 contiguous values share an E8M0 scale,
 // elements are E4M3FN.
-// The codec itself (integer-only, bit-exact) is in mx_codec.h.
+// The codec itself is in mx_codec.h.
 #include "common.h"
 #include "mx_codec.h"
 #include "kernels.h"

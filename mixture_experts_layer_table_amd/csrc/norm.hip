@@ -16,9 +16,9 @@
 // One workgroup per row, the row in registers: one pass over memory, bound by
 // HBM. A thread holds CH chunks of 8 elements, chunk c = i * threads + thread, so
 // that 4 neighbouring lanes hold one 32-value MXFP8 block. Measured: forward
-// 16,384 x 7,168 with dropout, bf16 and MXFP8 rows out, 183 us for 1.06 GB
-// (5.8 TB/s; a large copy moves 5.2), 2,048 x 7,168 in fp32 40 us (4.8 TB/s), one
-// row 2.5 us; backward 16,384 x 7,168 181 us for 940 MB (5.2 TB/s), 777 x 4,096 in
+// 16,384 x 7,168 with dropout, bf16 and MXFP8 rows out, 185 us for 1.06 GB
+// (5.7 TB/s; a large copy moves 5.2), 2,048 x 7,168 in fp32 41 us (4.7 TB/s), one
+// row 2.6 us; backward 16,384 x 7,168 181 us for 940 MB (5.2 TB/s), 777 x 4,096 in
 // fp32 with dropout 16 us (3.3 TB/s: two short kernels).
 #include <algorithm>
 #include <type_traits>

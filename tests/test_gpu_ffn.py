@@ -25,7 +25,8 @@ TOL_MX = 1e-2
 
 # rows around 1, 32, 128 and 256 (MFMA blocks and tile heights), widths below, at and past one tile, long
 # contraction axes (split) and short ones; BF16 takes multiples of 64, MXFP8 of 128
-# four rows and fewer take kernels of their own: 2 and 4 rows, run lengths and strips that do not divide evenly
+# one and two rows take kernels of their own (more of them in test_gpu_ffn_few.py): run lengths and strips that do not
+# divide evenly; the shapes that take each tile kernel are in test_gpu_ffn_tiles.py
 SHAPES_BF16 = [(1, 64, 64), (1, 1024, 512), (3, 192, 320), (2, 320, 192), (4, 2112, 1088), (1, 7168, 2048),
                (4, 128, 4096), (2, 5120, 64), (31, 128, 64), (33, 640, 192), (128, 512, 448),
                (129, 320, 128), (257, 256, 640), (300, 1088, 576), (700, 64, 1024), (65, 4096, 128), (5, 7168, 2048)]
