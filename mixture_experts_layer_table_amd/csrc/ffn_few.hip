@@ -15,7 +15,8 @@
 // Sums run in a fixed order: lane, wave, run.
 //
 // Measured, one row of 7,168 x 2,048: BF16 23 to 25 us over several cards (gate/up
-// 13, down 10), MXFP8 16 (9 and 6), two rows in MXFP8 21. Each kernel's launch, first loads and lane sums are 4 to 5 us.
+// 13, down 10), MXFP8 16 (9 and 6), two rows in MXFP8 21. Each kernel's
+// launch, first loads and lane sums are 4 to 5 us.
 //
 // Which calls come here is plan_few's rule (ffn_plan.cpp). The cost that grows
 // with the rows is each lane's sums, not the weights: at 7,168 x 2,048 two BF16

@@ -12,10 +12,11 @@
 // to 1,570 TFLOP/s; its gate/up product has 128 tiles of 256 rows for 256 compute
 // units: 128-row tiles instead, 71 us on one card, where 256 rows cut in two took 62
 // and their join 15), 16,384 rows 0.69 ms (2,100; 0.74 with an addend); backward
-// 16,384 rows 1.88 to 1.92 ms, of which the BF16 weight gradients are half the flops. A 128-row tile takes 0.5 to 0.6 us a K-step where
-// the 256-row one takes 0.8, so it pays where it saves a split or a round. Both
-// wait for their operands (2,048 rows' gate/up: 68 us; 64 without the MFMAs, 49
-// without the loads, 68 without the fragment reads).
+// 16,384 rows 1.88 to 1.92 ms, of which the BF16 weight gradients are half the flops.
+// A 128-row tile takes 0.5 to 0.6 us a K-step where the 256-row one takes 0.8, so it
+// pays where it saves a split or a round. Both wait for their operands (2,048 rows'
+// gate/up: 68 us on the fastest card; 64 without the MFMAs, 49 without the loads, 68
+// without the fragment reads).
 #include "ffn_parts.h"
 #include "gemm8.h"
 #include "kernels.h"
