@@ -1,9 +1,10 @@
 """The routed experts taken apart, case by case: token rows sorted by expert
 and back with their gate weights (and both gradients), quantization to 8-bit
 floating point with one fp32 scale for each block of 128 values (activation rows
-1 x 128, weights 128 x 128, either orientation, optionally of the gated
-activation silu(g) * u, whose gradient goes with it), and the matrix products on
-such operands: dense, grouped by expert, and the weight gradients.
+1 x 128 with scales [K / 128, rows], weights 128 x 128 with scales
+[rows / 128, K / 128], either orientation, optionally of the gated activation
+silu(g) * u, whose gradient goes with it), and the matrix products on such
+operands: dense, grouped by expert, and the weight gradients.
 
 ``run`` computes a case in its plain form (elementary torch operations in 32
 bits, one rounding at the end) or, with ``own`` set, through the library's
@@ -172,7 +173,7 @@ def prepare(case, seed):
             # the rows' buffers, made once: what lies behind the last expert's rows stays as it is
             if case["fp8"]:
                 s["buffers"] = dict(elems=torch.zeros(cap, H, dtype=torch.uint8, device=DEV),
-                                    scales=torch.zeros(cap, -(-H // BLK), device=DEV))
+                                    scales=torch.zeros(-(-H // BLK), cap, device=DEV))
             else:
                 s["buffers"] = dict(rows=torch.zeros(cap, H, dtype=dt, device=DEV))
             return s
@@ -259,16 +260,16 @@ def _to_codes(v, r, fine):
 
 
 def _codes_rows(v):
-    """E4M3 codes [.., K] and scales [.., K/128] of v, 128 values along the last axis a block (bytes)."""
+    """E4M3 codes [.., rows, K] (bytes) and scales [.., K/128, rows] of v, 128 values along the last axis a block."""
     b = _blocks(v.float(), -1)
     amax = b.abs().amax(-1)
     sc, r, fine = _scale_of(torch.where(torch.isfinite(b).all(-1), amax, float("nan")))
     q = _to_codes(b, r[..., None], fine[..., None]).view(torch.uint8).flatten(-2)[..., :v.shape[-1]].contiguous()
-    return q, sc
+    return q, sc.mT.contiguous()
 
 
 def _codes_tiles(v):
-    """The same with 128 x 128 blocks over the last two axes: scales [.., rows/128, K/128]."""
+    """Codes and scales [.., rows/128, K/128] of 128 x 128 blocks over the last two axes."""
     b = _blocks(_blocks(v.float(), -1), -3)                      # [.., rb, 128, kb, 128]
     amax = b.abs().amax((-3, -1))
     sc, r, fine = _scale_of(torch.where(torch.isfinite(b).all(-1).all(-2), amax, float("nan")))
@@ -279,7 +280,7 @@ def _codes_tiles(v):
 
 def _values_rows(codes):
     q, sc = codes
-    return q.view(torch.float8_e4m3fn).float() * sc.repeat_interleave(BLK, -1)[..., :q.shape[-1]]
+    return q.view(torch.float8_e4m3fn).float() * sc.mT.repeat_interleave(BLK, -1)[..., :q.shape[-1]]
 
 
 def _values_tiles(codes):
@@ -319,8 +320,8 @@ def _plain_permute(s):
     q, sc = _codes_rows(s["x"])
     # a padding row holds zeros, whose scale is the smallest
     pad = (torch.arange(cap, device=q.device) < sort["offsets"][-1]) & (sort["row_slots"] < 0)
-    scales = _into_rows(sc.unsqueeze(1).expand(-1, k, -1), sort["slots"], cap)
-    scales = torch.where(pad[:, None], LEAST / 448.0, scales)
+    scales = _into_rows(sc.mT.unsqueeze(1).expand(-1, k, -1), sort["slots"], cap)
+    scales = torch.where(pad[:, None], LEAST / 448.0, scales).mT.contiguous()
     out.update(_typed(_into_rows(q.unsqueeze(1).expand(-1, k, -1), sort["slots"], cap), scales))
     return out
 
@@ -442,7 +443,7 @@ def _x_codes(v, tile):
         full = full[:, torch.arange(n, device=v.device) // BLK]
     u = (v * 448.0 / full).clamp(-448.0, 448.0)
     step = torch.ldexp(torch.ones_like(u), (torch.frexp(u)[1] - 1).clamp(min=-6) - 3)   # E4M3's spacing at u
-    return torch.round(u / step) * step, m / 448.0
+    return torch.round(u / step) * step, m / 448.0 if tile else (m / 448.0).movedim(2, 1)
 
 
 def _x_e4m3(q):
@@ -455,7 +456,7 @@ def _x_e4m3(q):
 def _x_rows(codes):
     q, sc = codes
     kb = torch.arange(q.shape[-1], device=q.device) // BLK
-    return _x_e4m3(q) * sc.double()[..., kb]
+    return _x_e4m3(q) * sc.double().movedim(-2, -1)[..., kb]
 
 
 def _x_tiles(codes):
@@ -493,7 +494,7 @@ def exact(case, seed):
             return out
         q, sc = _x_codes(x[None], False)
         out["elems"] = torch.where((src >= 0)[:, None], q[0][at], 0.0)
-        out["scales"] = torch.where((src >= 0)[:, None], sc[0][at], torch.where(inside, LEAST / 448.0, 0.0)[:, None])
+        out["scales"] = torch.where(src >= 0, sc[0][:, at], torch.where(inside, LEAST / 448.0, 0.0))
         return out
     if op in ("permute_bwd", "unpermute"):
         slots, y = s["sort"]["slots"].long(), s["y"].double()
