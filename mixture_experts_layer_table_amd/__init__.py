@@ -14,6 +14,9 @@ project summary, Functional API and Key-concepts table):
   ``backward``, ``mxfp8_quantize`` — allocate the caller-side buffers with
   torch and call the entry points above. Around the layer: ``dropout``,
   ``add_rmsnorm``, ``get_ffn_workspace``, ``ffn_forward`` and their backwards.
+  The routed experts taken apart: ``sort_tokens``, ``permute``, ``unpermute`` and
+  their backwards, ``fp8_quantize``, ``glu_backward``, ``fp8_matmul``,
+  ``fp8_wgrad``.
 """
 from __future__ import annotations
 
@@ -46,11 +49,15 @@ EXPORTS = ("mok_config_default", "mok_config_autosize", "mok_query_sizes", "mok_
            "mok_route_backward", "mok_status_string", "mok_kernel_timing_enable", "mok_kernel_timing_read",
            "mok_last_error", "mok_forward_noalloc", "mok_item_trace_enable", "mok_item_trace_read",
            "mok_dropout", "mok_dropout_backward", "mok_add_rmsnorm", "mok_add_rmsnorm_backward_size",
-           "mok_add_rmsnorm_backward", "mok_ffn_query_size", "mok_ffn_forward", "mok_ffn_backward")
+           "mok_add_rmsnorm_backward", "mok_ffn_query_size", "mok_ffn_forward", "mok_ffn_backward",
+           "mok_sort_tokens_size", "mok_sort_tokens", "mok_permute", "mok_permute_backward", "mok_unpermute",
+           "mok_unpermute_backward", "mok_fp8_quantize", "mok_glu_backward", "mok_fp8_matmul_size", "mok_fp8_matmul",
+           "mok_fp8_wgrad_size", "mok_fp8_wgrad")
 MOK_TRACE_FWD_GEMMS, MOK_TRACE_BWD_GEMMS, MOK_TRACE_WGRAD_GATE_UP, MOK_TRACE_WGRAD_DOWN, MOK_TRACE_OTHER = range(5)
 MOK_ITEM_TRACE_CAPACITY = 65536
 MOK_NOALLOC_SCRATCH_BYTES = 64 << 20
 MOK_STREAM_BF16, MOK_STREAM_F32 = 0, 1
+MOK_FP8_TURNED, MOK_FP8_TILE, MOK_FP8_GLU = 1, 2, 4
 
 
 class mok_config(ctypes.Structure):
@@ -80,6 +87,20 @@ class mok_norm_shape(ctypes.Structure):
 class mok_ffn_shape(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int32), ("I", ctypes.c_int32),
                 ("precision", ctypes.c_int32)]
+
+
+class mok_sort_shape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("k", ctypes.c_int32), ("E", ctypes.c_int32), ("align", ctypes.c_int32)]
+
+
+class mok_rows_shape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("rows", ctypes.c_int64), ("k", ctypes.c_int32), ("E", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class mok_fp8_shape(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("E", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32)]
 
 
 class mok_kernel_stat(ctypes.Structure):
@@ -133,6 +154,19 @@ _sigs = {
                         ctypes.POINTER(mok_weights), _P, _P, _P, _P],
     "mok_ffn_backward": [ctypes.POINTER(mok_ffn_shape), _P, ctypes.c_size_t, _P, ctypes.POINTER(mok_weights), _P, _P,
                          _P, _P, _P, _P, _P, _P],
+    "mok_sort_tokens_size": [ctypes.POINTER(mok_sort_shape), ctypes.POINTER(ctypes.c_int64), _sz],
+    "mok_sort_tokens": [ctypes.POINTER(mok_sort_shape), _P, ctypes.c_size_t, _P, _P, _P, _P, _P],
+    "mok_permute": [ctypes.POINTER(mok_rows_shape), _P, _P, _P, _P, _P, _P, _P, _P],
+    "mok_permute_backward": [ctypes.POINTER(mok_rows_shape), _P, _P, _P, _P],
+    "mok_unpermute": [ctypes.POINTER(mok_rows_shape), _P, _P, _P, _P, _P, _P],
+    "mok_unpermute_backward": [ctypes.POINTER(mok_rows_shape), _P, _P, _P, _P, _P, _P, _P, _P, _P],
+    "mok_fp8_quantize": [_P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_uint32, _P, _P,
+                         _P],
+    "mok_glu_backward": [_P, _P, ctypes.c_int64, ctypes.c_int32, _P, _P],
+    "mok_fp8_matmul_size": [ctypes.POINTER(mok_fp8_shape), _sz],
+    "mok_fp8_matmul": [ctypes.POINTER(mok_fp8_shape), _P, ctypes.c_size_t, _P, _P, _P, _P, _P, _P, _P],
+    "mok_fp8_wgrad_size": [ctypes.POINTER(mok_fp8_shape), _sz],
+    "mok_fp8_wgrad": [ctypes.POINTER(mok_fp8_shape), _P, ctypes.c_size_t, _P, _P, _P, _P, _P, _P, _P, _P],
     "mok_kernel_timing_enable": [ctypes.c_int32],
     "mok_item_trace_enable": [ctypes.c_int32],
     "mok_item_trace_read": [ctypes.POINTER(mok_item_record), ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)],
@@ -258,6 +292,58 @@ def mok_ffn_backward(shape, workspace, workspace_bytes, x, weights, h, dy, adden
                      stream):
     return _lib.mok_ffn_backward(ctypes.byref(shape), workspace, workspace_bytes, x, ctypes.byref(weights), h, dy,
                                  addend, dx, dw_gate, dw_up, dw_down, stream)
+
+
+def mok_sort_tokens_size(shape, rows, workspace):
+    return _lib.mok_sort_tokens_size(ctypes.byref(shape), rows, workspace)
+
+
+def mok_sort_tokens(shape, workspace, workspace_bytes, topk_ids, offsets, slots, row_slots, stream):
+    return _lib.mok_sort_tokens(ctypes.byref(shape), workspace, workspace_bytes, topk_ids, offsets, slots, row_slots,
+                                stream)
+
+
+def mok_permute(shape, x, offsets, slots, row_slots, rows, elems, scales, stream):
+    return _lib.mok_permute(ctypes.byref(shape), x, offsets, slots, row_slots, rows, elems, scales, stream)
+
+
+def mok_permute_backward(shape, drows, slots, dx, stream):
+    return _lib.mok_permute_backward(ctypes.byref(shape), drows, slots, dx, stream)
+
+
+def mok_unpermute(shape, y, slots, w, addend, out, stream):
+    return _lib.mok_unpermute(ctypes.byref(shape), y, slots, w, addend, out, stream)
+
+
+def mok_unpermute_backward(shape, dout, y, offsets, slots, row_slots, w, dy, dw, stream):
+    return _lib.mok_unpermute_backward(ctypes.byref(shape), dout, y, offsets, slots, row_slots, w, dy, dw, stream)
+
+
+def mok_fp8_quantize(src, dtype, batch, rows, K, flags, elems, scales, stream):
+    return _lib.mok_fp8_quantize(src, dtype, batch, rows, K, flags, elems, scales, stream)
+
+
+def mok_glu_backward(da, h, T, I, dh, stream):
+    return _lib.mok_glu_backward(da, h, T, I, dh, stream)
+
+
+def mok_fp8_matmul_size(shape, workspace):
+    return _lib.mok_fp8_matmul_size(ctypes.byref(shape), workspace)
+
+
+def mok_fp8_matmul(shape, workspace, workspace_bytes, a_elems, a_scales, b_elems, b_scales, offsets, out, stream):
+    return _lib.mok_fp8_matmul(ctypes.byref(shape), workspace, workspace_bytes, a_elems, a_scales, b_elems, b_scales,
+                               offsets, out, stream)
+
+
+def mok_fp8_wgrad_size(shape, workspace):
+    return _lib.mok_fp8_wgrad_size(ctypes.byref(shape), workspace)
+
+
+def mok_fp8_wgrad(shape, workspace, workspace_bytes, dy_elems, dy_scales, x_elems, x_scales, offsets, addend, out,
+                  stream):
+    return _lib.mok_fp8_wgrad(ctypes.byref(shape), workspace, workspace_bytes, dy_elems, dy_scales, x_elems, x_scales,
+                              offsets, addend, out, stream)
 
 
 def mok_kernel_timing_enable(enable):
@@ -925,6 +1011,363 @@ def ffn_backward(ws: FfnWorkspace, x, weights: mok_weights, h, dy, addend=None, 
                                  g["dx"].data_ptr(), g["dw_gate"].data_ptr(), g["dw_up"].data_ptr(),
                                  g["dw_down"].data_ptr(), _raw_stream(dev.index)), "mok_ffn_backward")
     return g
+
+
+# ----------------------------------------------------------------------------- the routed experts taken apart
+
+_I32 = torch.int32
+_rows_shape = functools.lru_cache(256)(mok_rows_shape)
+_fp8_shape = functools.lru_cache(256)(mok_fp8_shape)
+
+
+@functools.lru_cache(256)
+def _sort_sizes(T, k, E, align):
+    shape, rows, need = mok_sort_shape(T, k, E, align), ctypes.c_int64(), ctypes.c_size_t()
+    _check(mok_sort_tokens_size(shape, ctypes.byref(rows), ctypes.byref(need)), "mok_sort_tokens_size")
+    return shape, rows.value, need.value
+
+
+@functools.lru_cache(256)
+def _fp8_bytes(wgrad, M, N, K, E, dtype) -> int:
+    need = ctypes.c_size_t()
+    size, name = (mok_fp8_wgrad_size, "mok_fp8_wgrad_size") if wgrad else (mok_fp8_matmul_size, "mok_fp8_matmul_size")
+    _check(size(mok_fp8_shape(M, N, K, E, dtype), ctypes.byref(need)), name)
+    return need.value
+
+
+def _given_workspace(workspace, need, like):
+    if workspace is None:
+        return like.new_empty((need,), dtype=_U8)
+    _require_bytes(workspace, "workspace", need, like.device)
+    return workspace
+
+
+def sort_rows(num_tokens: int, topk: int, num_experts: int, align: int = 1) -> int:
+    """Most rows that a sort of these sizes fills (mok_sort_tokens_size)."""
+    return _sort_sizes(num_tokens, topk, num_experts, align)[1]
+
+
+def sort_tokens(topk_ids, num_experts: int, align: int = 1, outs=None, workspace=None):
+    """Sort of token slots by expert (mok_sort_tokens). topk_ids: int32 [T, k]; an
+    id outside [0, num_experts) names no expert here. Every expert's run of rows
+    is rounded up to a multiple of ``align``. Returns a dict of int32 tensors:
+    offsets [E + 1], slots [T, k] (each slot's row, or -1) and row_slots [rows]
+    (each row's slot t * k + j, or -1), rows as sort_rows() gives. ``outs``: the
+    same keys, caller-given; ``workspace``: uint8, made here if None."""
+    shape, dev = topk_ids.shape, topk_ids.device
+    if len(shape) != 2:
+        raise ValueError(f"topk_ids: shape {tuple(shape)}, expected [T, k]")
+    T, k = shape
+    _need(topk_ids, "topk_ids", _I32, shape, dev)
+    c, rows, need = _sort_sizes(T, k, num_experts, align)
+    if outs is not None:
+        _need(outs.get("offsets"), "offsets", _I32, (num_experts + 1,), dev)
+        _need(outs.get("slots"), "slots", _I32, shape, dev)
+        _need(outs.get("row_slots"), "row_slots", _I32, (rows,), dev)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return sort_tokens(topk_ids, num_experts, align, outs, workspace)
+    ws = _given_workspace(workspace, need, topk_ids)
+    if outs is None:
+        r = dict(offsets=topk_ids.new_empty((num_experts + 1,)), slots=torch.empty_like(topk_ids),
+                 row_slots=topk_ids.new_empty((rows,)))
+    else:
+        r = {n: outs[n] for n in ("offsets", "slots", "row_slots")}
+    _check(_lib.mok_sort_tokens(ctypes.byref(c), ws.data_ptr(), ws.numel(), topk_ids.data_ptr(),
+                                r["offsets"].data_ptr(), r["slots"].data_ptr(), r["row_slots"].data_ptr(),
+                                _raw_stream(dev.index)), "mok_sort_tokens")
+    return r
+
+
+def _sort_of(sort, device):
+    """(T, k, rows, E) of a sort_tokens() dict, its tensors checked."""
+    slots, row_slots, offsets = sort["slots"], sort["row_slots"], sort["offsets"]
+    if slots.dim() != 2 or row_slots.dim() != 1 or offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("sort: expected slots [T, k], row_slots [rows] and offsets [E + 1]")
+    _need(slots, "slots", _I32, slots.shape, device)
+    _need(row_slots, "row_slots", _I32, row_slots.shape, device)
+    _need(offsets, "offsets", _I32, offsets.shape, device)
+    return slots.shape[0], slots.shape[1], row_slots.shape[0], offsets.shape[0] - 1
+
+
+def _rows_of(t, name, n, dtype=None, device=None):
+    """H of a tensor of n rows, checked."""
+    if t.dim() != 2 or t.shape[0] != n:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{n}, H]")
+    _need(t, name, t.dtype if dtype is None else dtype, t.shape, t.device if device is None else device)
+    return t.shape[1]
+
+
+def permute(x, sort, rows: bool = True, fp8: bool = False, outs=None):
+    """Token rows into their experts' order (mok_permute). x: bf16 or fp32 [T, H];
+    sort: what sort_tokens() returned. Returns a dict: rows [rows, H] in x's type
+    (if ``rows``), elems uint8 [rows, H] and scales fp32 [ceil(H/128), rows] (if
+    ``fp8``: the rows quantized in blocks of 128). Rows behind the last expert's
+    run are not written. ``outs``: the same keys, caller-given."""
+    dev = x.device
+    sd = _stream_dtype(x.dtype, "x")
+    T, k, n, E = _sort_of(sort, dev)
+    H = _rows_of(x, "x", T)
+    if not rows and not fp8:
+        raise ValueError("rows and fp8 are both off: nothing to write")
+    if H % 8 or (fp8 and H % 16):
+        raise ValueError(f"x: H = {H}, expected a multiple of {16 if fp8 else 8}")
+    kb = (H + 127) // 128
+    if outs is not None:
+        if rows:
+            _need(outs.get("rows"), "rows", x.dtype, (n, H), dev)
+        if fp8:
+            _need(outs.get("elems"), "elems", _U8, (n, H), dev)
+            _need(outs.get("scales"), "scales", _F32, (kb, n), dev)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return permute(x, sort, rows, fp8, outs)
+    if outs is None:
+        r = dict(rows=x.new_empty((n, H))) if rows else {}
+        if fp8:
+            r["elems"], r["scales"] = x.new_empty((n, H), dtype=_U8), x.new_empty((kb, n), dtype=_F32)
+    else:
+        r = {name: outs[name] for name in (("rows",) if rows else ()) + (("elems", "scales") if fp8 else ())}
+    _check(_lib.mok_permute(ctypes.byref(_rows_shape(T, n, k, E, H, sd)), x.data_ptr(), sort["offsets"].data_ptr(),
+                            sort["slots"].data_ptr(), sort["row_slots"].data_ptr(), _addr(r.get("rows")),
+                            _addr(r.get("elems")), _addr(r.get("scales")), _raw_stream(dev.index)), "mok_permute")
+    return r
+
+
+def permute_backward(drows, sort, dx=None):
+    """Gradient of permute() with respect to x (mok_permute_backward): the sum of
+    each token's rows. drows: bf16 or fp32 [rows, H]. Returns [T, H] in its type."""
+    dev = drows.device
+    sd = _stream_dtype(drows.dtype, "drows")
+    T, k, n, E = _sort_of(sort, dev)
+    H = _rows_of(drows, "drows", n)
+    if dx is not None:
+        _need(dx, "dx", drows.dtype, (T, H), dev)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return permute_backward(drows, sort, dx)
+    if dx is None:
+        dx = drows.new_empty((T, H))
+    _check(_lib.mok_permute_backward(ctypes.byref(_rows_shape(T, n, k, E, H, sd)), drows.data_ptr(),
+                                     sort["slots"].data_ptr(), dx.data_ptr(), _raw_stream(dev.index)),
+           "mok_permute_backward")
+    return dx
+
+
+def unpermute(y, sort, w=None, addend=None, out=None):
+    """The experts' rows back in token order (mok_unpermute): out[t] = addend[t] +
+    sum over j of w[t, j] * y[slots[t, j]]. y: bf16 or fp32 [rows, H]; w: fp32
+    [T, k] or None (ones); addend: [T, H] in y's type or None (its gradient is
+    out's). ``out`` may be addend."""
+    dev = y.device
+    sd = _stream_dtype(y.dtype, "y")
+    T, k, n, E = _sort_of(sort, dev)
+    H = _rows_of(y, "y", n)
+    if w is not None:
+        _need(w, "w", _F32, (T, k), dev)
+    if addend is not None:
+        _need(addend, "addend", y.dtype, (T, H), dev)
+    if out is not None:
+        _need(out, "out", y.dtype, (T, H), dev)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return unpermute(y, sort, w, addend, out)
+    if out is None:
+        out = y.new_empty((T, H))
+    _check(_lib.mok_unpermute(ctypes.byref(_rows_shape(T, n, k, E, H, sd)), y.data_ptr(), sort["slots"].data_ptr(),
+                              _addr(w), _addr(addend), out.data_ptr(), _raw_stream(dev.index)), "mok_unpermute")
+    return out
+
+
+def unpermute_backward(dout, y, sort, w, grads=None):
+    """Gradient of unpermute() with weights (mok_unpermute_backward). dout: [T, H],
+    y: [rows, H] in the same type, as the forward read it; w: fp32 [T, k]. Returns
+    dict(dy [rows, H], dw fp32 [T, k]); rows behind the last expert's run are not
+    written. ``grads``: the same keys, caller-given (dy may be y). Without weights
+    the gradient is permute(dout, sort)."""
+    dev = y.device
+    sd = _stream_dtype(y.dtype, "y")
+    T, k, n, E = _sort_of(sort, dev)
+    H = _rows_of(y, "y", n)
+    _need(dout, "dout", y.dtype, (T, H), dev)
+    _need(w, "w", _F32, (T, k), dev)
+    if grads is not None:
+        _need(grads.get("dy"), "dy", y.dtype, (n, H), dev)
+        _need(grads.get("dw"), "dw", _F32, (T, k), dev)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return unpermute_backward(dout, y, sort, w, grads)
+    g = dict(dy=torch.empty_like(y), dw=torch.empty_like(w)) if grads is None else dict(dy=grads["dy"], dw=grads["dw"])
+    _check(_lib.mok_unpermute_backward(ctypes.byref(_rows_shape(T, n, k, E, H, sd)), dout.data_ptr(), y.data_ptr(),
+                                       sort["offsets"].data_ptr(), sort["slots"].data_ptr(),
+                                       sort["row_slots"].data_ptr(), w.data_ptr(), g["dy"].data_ptr(),
+                                       g["dw"].data_ptr(), _raw_stream(dev.index)), "mok_unpermute_backward")
+    return g
+
+
+def fp8_quantize(src, src_is_k_by_rows: bool = False, tile: bool = False, glu: bool = False, outs=None):
+    """Quantization to E4M3 with one fp32 scale per block of 128 (mok_fp8_quantize).
+    src: bf16 or fp32 [B, rows, K], or [B, K, rows] when src_is_k_by_rows
+    (quantizes the transpose). A block is 128 values along K, or with ``tile`` 128
+    rows x 128 values. With ``glu`` (bf16, no tile) src is [.., 2K] (or [B, K,
+    2 * rows]) and silu(g) * u of its halves is quantized. Returns (elems uint8
+    [B, rows, K], scales fp32 [B, ceil(K/128), rows], or with ``tile``
+    [B, ceil(rows/128), ceil(K/128)]); ``outs``: such a pair, caller-given."""
+    dev = src.device
+    if src.dim() != 3:
+        raise ValueError(f"src: expected [B, rows, K] or [B, K, rows], got shape {tuple(src.shape)}")
+    sd = _stream_dtype(src.dtype, "src")
+    _need(src, "src", src.dtype, src.shape, dev)
+    B, last = src.shape[0], src.shape[2]
+    if glu:
+        if tile or sd != MOK_STREAM_BF16:
+            raise ValueError("glu takes bf16 rows and no tile")
+        if last % 2:
+            raise ValueError(f"src: last dimension {last}, expected two halves")
+        last //= 2
+    rows, K = (last, src.shape[1]) if src_is_k_by_rows else (src.shape[1], last)
+    if K % 16 or (src_is_k_by_rows and rows % 8):
+        raise ValueError(f"src: K = {K}, rows = {rows}: K must be a multiple of 16"
+                         + (" and rows of 8" if src_is_k_by_rows else ""))
+    kb = (K + 127) // 128
+    sshape = (B, (rows + 127) // 128, kb) if tile else (B, kb, rows)
+    if outs is not None:
+        if not isinstance(outs, (tuple, list)) or len(outs) != 2:
+            raise ValueError("outs: expected (elems, scales)")
+        _need(outs[0], "elems", _U8, (B, rows, K), dev)
+        _need(outs[1], "scales", _F32, sshape, dev)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return fp8_quantize(src, src_is_k_by_rows, tile, glu, outs)
+    elems, scales = (src.new_empty((B, rows, K), dtype=_U8), src.new_empty(sshape, dtype=_F32)) if outs is None else outs
+    flags = (MOK_FP8_TURNED if src_is_k_by_rows else 0) | (MOK_FP8_TILE if tile else 0) | (MOK_FP8_GLU if glu else 0)
+    _check(_lib.mok_fp8_quantize(src.data_ptr(), sd, B, rows, K, flags, elems.data_ptr(), scales.data_ptr(),
+                                 _raw_stream(dev.index)), "mok_fp8_quantize")
+    return elems, scales
+
+
+def glu_backward(da, h, dh=None):
+    """Gradient of a = silu(g) * u with respect to h = [g | u] (mok_glu_backward).
+    da: bf16 [T, I], h: bf16 [T, 2I]. Returns bf16 [T, 2I]; ``dh`` may be h."""
+    dev = da.device
+    if da.dim() != 2 or da.shape[1] % 8:
+        raise ValueError(f"da: shape {tuple(da.shape)}, expected [T, I] with I a multiple of 8")
+    T, I = da.shape
+    _need(da, "da", _BF16, (T, I), dev)
+    _need(h, "h", _BF16, (T, 2 * I), dev)
+    if dh is not None:
+        _need(dh, "dh", _BF16, (T, 2 * I), dev)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return glu_backward(da, h, dh)
+    if dh is None:
+        dh = torch.empty_like(h)
+    _check(_lib.mok_glu_backward(da.data_ptr(), h.data_ptr(), T, I, dh.data_ptr(), _raw_stream(dev.index)),
+           "mok_glu_backward")
+    return dh
+
+
+def _pair(t, name):
+    if not isinstance(t, (tuple, list)) or len(t) != 2:
+        raise ValueError(f"{name}: expected (elems, scales)")
+    return t
+
+
+def _row_codes(t, name, device=None):
+    """(elems, scales, rows, K) of rows quantized in blocks of 128, with or without a leading dimension of 1."""
+    el, sc = _pair(t, name)
+    if el.dim() == 3 and el.shape[0] == 1 and sc.dim() == 3:
+        el, sc = el[0], sc[0]
+    if el.dim() != 2:
+        raise ValueError(f"{name} elems: shape {tuple(el.shape)}, expected [rows, K]")
+    dev = el.device if device is None else device
+    _need(el, name + " elems", _U8, el.shape, dev)
+    _need(sc, name + " scales", _F32, ((el.shape[1] + 127) // 128, el.shape[0]), dev)
+    return el, sc, el.shape[0], el.shape[1]
+
+
+def _experts(offsets, device):
+    if offsets is None:
+        return 0
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError(f"offsets: shape {tuple(offsets.shape)}, expected [E + 1]")
+    _need(offsets, "offsets", _I32, offsets.shape, device)
+    return offsets.shape[0] - 1
+
+
+def fp8_matmul(a, b, offsets=None, out_dtype=torch.bfloat16, out=None, workspace=None):
+    """a @ b^T on operands in blocks of 128 (mok_fp8_matmul). a: (elems uint8
+    [M, K], scales fp32 [ceil(K/128), M]), rows of fp8_quantize or permute; b:
+    (elems uint8 [N, K], scales fp32 [ceil(N/128), ceil(K/128)]), tiles. With
+    ``offsets`` (int32 [E + 1] on the device, as sort_tokens returns them) b has a
+    leading dimension E and rows [offsets[e], offsets[e + 1]) meet b[e]; rows of
+    no expert are not written. Returns bf16 or fp32 [M, N]; ``out``: caller-given,
+    in the type it has. N and K are multiples of 16."""
+    el, sc, M, K = _row_codes(a, "a")
+    dev = el.device
+    E = _experts(offsets, dev)
+    bel, bsc = _pair(b, "b")
+    if E == 0 and bel.dim() == 3 and bel.shape[0] == 1 and bsc.dim() == 3:
+        bel, bsc = bel[0], bsc[0]
+    if bel.dim() != (3 if E else 2):
+        raise ValueError(f"b elems: shape {tuple(bel.shape)}, expected " + ("[E, N, K]" if E else "[N, K]"))
+    N = bel.shape[-2]
+    lead = (E,) if E else ()
+    _need(bel, "b elems", _U8, lead + (N, K), dev)
+    _need(bsc, "b scales", _F32, lead + ((N + 127) // 128, (K + 127) // 128), dev)
+    if N % 16 or K % 16:
+        raise ValueError(f"N = {N}, K = {K}: expected multiples of 16")
+    if out is not None:
+        out_dtype = out.dtype
+        _need(out, "out", out_dtype, (M, N), dev)
+    sd = _stream_dtype(out_dtype, "out")
+    need = _fp8_bytes(False, M, N, K, E, sd)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return fp8_matmul(a, b, offsets, out_dtype, out, workspace)
+    ws = _given_workspace(workspace, need, el)
+    if out is None:
+        out = el.new_empty((M, N), dtype=out_dtype)
+    _check(_lib.mok_fp8_matmul(ctypes.byref(_fp8_shape(M, N, K, E, sd)), ws.data_ptr(), ws.numel(), el.data_ptr(),
+                               sc.data_ptr(), bel.data_ptr(), bsc.data_ptr(), _addr(offsets), out.data_ptr(),
+                               _raw_stream(dev.index)), "mok_fp8_matmul")
+    return out
+
+
+def fp8_wgrad(dy, x, offsets=None, out_dtype=torch.bfloat16, addend=None, out=None, workspace=None):
+    """Weight gradient addend + dy^T x over the rows of each expert (mok_fp8_wgrad).
+    dy: (elems uint8 [N, R], scales fp32 [ceil(R/128), N]), x: (elems uint8 [K, R],
+    scales fp32 [ceil(R/128), K]), both from fp8_quantize(.., src_is_k_by_rows=True)
+    of the R rows. ``offsets``: int32 [E + 1] whose runs start at multiples of 128
+    (sort_tokens with align=128), or None for one product. Returns [E, N, K] or
+    [N, K] in bf16 or fp32; ``addend`` and ``out`` have that shape, and ``out``
+    may be addend. N, K and R are multiples of 16."""
+    el, sc, N, R = _row_codes(dy, "dy")
+    dev = el.device
+    xel, xsc, K, R2 = _row_codes(x, "x", dev)
+    if R2 != R:
+        raise ValueError(f"x elems: {R2} rows along the contraction, dy has {R}")
+    if N % 16 or K % 16 or R % 16:
+        raise ValueError(f"N = {N}, K = {K}, R = {R}: expected multiples of 16")
+    E = _experts(offsets, dev)
+    shape = ((E,) if E else ()) + (N, K)
+    if out is not None:
+        out_dtype = out.dtype
+        _need(out, "out", out_dtype, shape, dev)
+    sd = _stream_dtype(out_dtype, "out")
+    if addend is not None:
+        _need(addend, "addend", out_dtype, shape, dev)
+    need = _fp8_bytes(True, R, N, K, E, sd)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return fp8_wgrad(dy, x, offsets, out_dtype, addend, out, workspace)
+    ws = _given_workspace(workspace, need, el)
+    if out is None:
+        out = el.new_empty(shape, dtype=out_dtype)
+    _check(_lib.mok_fp8_wgrad(ctypes.byref(_fp8_shape(R, N, K, E, sd)), ws.data_ptr(), ws.numel(), el.data_ptr(),
+                              sc.data_ptr(), xel.data_ptr(), xsc.data_ptr(), _addr(offsets), _addr(addend),
+                              out.data_ptr(), _raw_stream(dev.index)), "mok_fp8_wgrad")
+    return out
 
 
 def read_schedule(schedule, layout: mok_schedule_layout, E: int):

@@ -3,6 +3,7 @@
 #include <cstdint>
 
 #include "ffn_plan.h"
+#include "fp8_plan.h"
 #include "kernels.h"
 #include "plan.h"
 
@@ -428,6 +429,213 @@ mok_status mok_ffn_backward(const mok_ffn_shape *shape, void *workspace, size_t 
                                static_cast<uint16_t *>(dx), static_cast<uint16_t *>(dw_gate),
                                static_cast<uint16_t *>(dw_up), static_cast<uint16_t *>(dw_down),
                                static_cast<hipStream_t>(stream));
+}
+
+mok_status mok_sort_tokens_size(const mok_sort_shape *shape, int64_t *rows, size_t *workspace_bytes) {
+    SortPlan p;
+    if (!shape || !sort_plan(shape->T, shape->k, shape->E, shape->align, &p)) return MOK_ERROR_INVALID_VALUE;
+    if (rows) *rows = p.rows;
+    if (workspace_bytes) *workspace_bytes = p.bytes;
+    return MOK_OK;
+}
+
+mok_status mok_sort_tokens(const mok_sort_shape *shape, void *workspace, size_t workspace_bytes,
+                           const int32_t *topk_ids, int32_t *offsets, int32_t *slots, int32_t *row_slots,
+                           void *stream) {
+    SortPlan p;
+    if (!shape || !sort_plan(shape->T, shape->k, shape->E, shape->align, &p)) return MOK_ERROR_INVALID_VALUE;
+    if (!dev_ok(workspace) || !dev_ok(offsets)) return MOK_ERROR_INVALID_VALUE;
+    if (p.n > 0 && (!dev_ok(topk_ids) || !dev_ok(slots) || !dev_ok(row_slots))) return MOK_ERROR_INVALID_VALUE;
+    if (workspace_bytes < p.bytes) return MOK_ERROR_BUFFER_TOO_SMALL;
+    const size_t n = (size_t)p.n * 4;
+    const Span outs[] = {{offsets, ((size_t)shape->E + 1) * 4}, {slots, n}, {row_slots, (size_t)p.rows * 4},
+                         {workspace, p.bytes}};
+    const Span ins[] = {{topk_ids, n}};
+    if (!apart(outs)) return MOK_ERROR_INVALID_VALUE;
+    for (const Span &o : outs)
+        if (any_overlap(o, ins)) return MOK_ERROR_INVALID_VALUE;
+    (void)hipGetLastError();
+    return launch_sort_tokens(p, shape->E, shape->align, topk_ids, workspace, offsets, slots, row_slots,
+                              static_cast<hipStream_t>(stream));
+}
+
+static bool rows_shape_ok(const mok_rows_shape *s) {
+    const int64_t lim = int64_t(1) << 31;
+    return s && s->T >= 0 && s->T < lim && s->rows >= 0 && s->rows < lim && s->k >= 1 && s->T * s->k < lim &&
+           s->E >= 1 && s->E <= 4096 && s->H > 0 && s->H % 8 == 0 && s->H <= (1 << 20) && stream_ok(s->dtype);
+}
+static RowsCall rows_call(const mok_rows_shape *s, const int32_t *offsets, const int32_t *slots,
+                          const int32_t *row_slots) {
+    return RowsCall{s->T, s->rows, s->k, s->E, s->H, s->dtype == MOK_STREAM_F32, offsets, slots, row_slots};
+}
+// Bytes of the tensors that a shape describes.
+struct RowsSizes {
+    size_t token, row, slot, row_slot, offset;
+    explicit RowsSizes(const mok_rows_shape *s)
+        : token((size_t)s->T * s->H * (s->dtype == MOK_STREAM_F32 ? 4 : 2)),
+          row((size_t)s->rows * s->H * (s->dtype == MOK_STREAM_F32 ? 4 : 2)), slot((size_t)s->T * s->k * 4),
+          row_slot((size_t)s->rows * 4), offset(((size_t)s->E + 1) * 4) {}
+};
+
+mok_status mok_permute(const mok_rows_shape *shape, const void *x, const int32_t *offsets, const int32_t *slots,
+                       const int32_t *row_slots, void *rows, uint8_t *elems, float *scales, void *stream) {
+    if (!rows_shape_ok(shape)) return MOK_ERROR_INVALID_VALUE;
+    if (shape->rows == 0) return MOK_OK;
+    if ((elems == nullptr) != (scales == nullptr) || (!rows && !elems)) return MOK_ERROR_INVALID_VALUE;
+    if (elems && shape->H % 16) return MOK_ERROR_INVALID_VALUE;
+    if (!dev_ok(offsets) || !dev_ok(row_slots) || !dev_ok_or_null(rows) || !dev_ok_or_null(elems) ||
+        !dev_ok_or_null(scales) || (shape->T > 0 && (!dev_ok(x) || !dev_ok(slots))))
+        return MOK_ERROR_INVALID_VALUE;
+    const RowsSizes n(shape);
+    const size_t ne = (size_t)shape->rows * shape->H, ns = (size_t)shape->rows * ((shape->H + 127) / 128) * 4;
+    const Span outs[] = {{rows, n.row}, {elems, ne}, {scales, ns}};
+    const Span ins[] = {{x, n.token}, {offsets, n.offset}, {slots, n.slot}, {row_slots, n.row_slot}};
+    if (!apart(outs)) return MOK_ERROR_INVALID_VALUE;
+    for (const Span &o : outs)
+        if (any_overlap(o, ins)) return MOK_ERROR_INVALID_VALUE;
+    (void)hipGetLastError();
+    return launch_permute(rows_call(shape, offsets, slots, row_slots), x, rows, elems, scales,
+                          static_cast<hipStream_t>(stream));
+}
+
+static mok_status unpermute(const mok_rows_shape *shape, const void *y, const int32_t *slots, const float *w,
+                            const void *addend, void *out, const char *where, void *stream) {
+    if (!rows_shape_ok(shape)) return MOK_ERROR_INVALID_VALUE;
+    if (shape->T == 0) return MOK_OK;
+    if (!dev_ok(slots) || !dev_ok_or_null(w) || !dev_ok_or_null(addend) || !dev_ok(out) ||
+        (shape->rows > 0 && !dev_ok(y)))
+        return MOK_ERROR_INVALID_VALUE;
+    const RowsSizes n(shape);
+    const Span so{out, n.token};
+    const Span ins[] = {{y, n.row}, {slots, n.slot}, {w, n.slot}};
+    if (any_overlap(so, ins) || overlap_partly(so, {addend, n.token})) return MOK_ERROR_INVALID_VALUE;
+    (void)hipGetLastError();
+    return launch_unpermute(rows_call(shape, nullptr, slots, nullptr), y, w, addend, out, where,
+                            static_cast<hipStream_t>(stream));
+}
+
+mok_status mok_permute_backward(const mok_rows_shape *shape, const void *drows, const int32_t *slots, void *dx,
+                                void *stream) {
+    return unpermute(shape, drows, slots, nullptr, nullptr, dx, "mok_permute_backward", stream);
+}
+
+mok_status mok_unpermute(const mok_rows_shape *shape, const void *y, const int32_t *slots, const float *w,
+                         const void *addend, void *out, void *stream) {
+    return unpermute(shape, y, slots, w, addend, out, "mok_unpermute", stream);
+}
+
+mok_status mok_unpermute_backward(const mok_rows_shape *shape, const void *dout, const void *y,
+                                  const int32_t *offsets, const int32_t *slots, const int32_t *row_slots,
+                                  const float *w, void *dy, float *dw, void *stream) {
+    if (!rows_shape_ok(shape)) return MOK_ERROR_INVALID_VALUE;
+    if (shape->T == 0 && shape->rows == 0) return MOK_OK;
+    if (shape->rows > 0 && (!dev_ok(y) || !dev_ok(dy) || !dev_ok(offsets) || !dev_ok(row_slots)))
+        return MOK_ERROR_INVALID_VALUE;
+    if (shape->T > 0 && (!dev_ok(dout) || !dev_ok(slots) || !dev_ok(w) || !dev_ok(dw))) return MOK_ERROR_INVALID_VALUE;
+    const RowsSizes n(shape);
+    const Span sdy{dy, n.row}, sdw{dw, n.slot}, sy{y, n.row};
+    const Span ins[] = {{dout, n.token}, {offsets, n.offset}, {slots, n.slot}, {row_slots, n.row_slot}, {w, n.slot}};
+    if (overlap(sdy, sdw) || any_overlap(sdy, ins) || any_overlap(sdw, ins) || overlap_partly(sdy, sy) ||
+        overlap(sdw, sy))
+        return MOK_ERROR_INVALID_VALUE;
+    (void)hipGetLastError();
+    return launch_unpermute_backward(rows_call(shape, offsets, slots, row_slots), dout, y, w, dy, dw,
+                                     static_cast<hipStream_t>(stream));
+}
+
+mok_status mok_fp8_quantize(const void *src, int32_t dtype, int64_t batch, int64_t rows, int64_t K, uint32_t flags,
+                            uint8_t *elems, float *scales, void *stream) {
+    const int64_t lim = int64_t(1) << 31;
+    const bool turned = flags & MOK_FP8_TURNED, tile = flags & MOK_FP8_TILE, glu = flags & MOK_FP8_GLU;
+    if (flags > (MOK_FP8_TURNED | MOK_FP8_TILE | MOK_FP8_GLU) || !stream_ok(dtype) || batch < 0 || batch >= 65536 ||
+        rows < 0 || rows >= lim || K < 0 || K >= lim || K % 16 || (turned && rows % 8))
+        return MOK_ERROR_INVALID_VALUE;
+    if (glu && (tile || dtype != MOK_STREAM_BF16)) return MOK_ERROR_INVALID_VALUE;
+    if (rows && K >= (int64_t(1) << 40) / rows) return MOK_ERROR_INVALID_VALUE;
+    if (batch * rows * K == 0) return MOK_OK;
+    if (!dev_ok(src) || !dev_ok(elems) || !dev_ok(scales)) return MOK_ERROR_INVALID_VALUE;
+    const size_t n = (size_t)batch * rows * K, kb = (size_t)(K + 127) / 128;
+    const Span outs[] = {{elems, n}, {scales, batch * kb * (tile ? (rows + 127) / 128 : rows) * 4}};
+    const Span in{src, n * (dtype == MOK_STREAM_F32 ? 4 : 2) * (glu ? 2 : 1)};
+    if (!apart(outs) || any_overlap(in, outs)) return MOK_ERROR_INVALID_VALUE;
+    (void)hipGetLastError();
+    return launch_fp8_quantize(src, dtype == MOK_STREAM_F32, batch, rows, K, flags, elems, scales,
+                               static_cast<hipStream_t>(stream));
+}
+
+mok_status mok_glu_backward(const void *da, const void *h, int64_t T, int32_t I, void *dh, void *stream) {
+    if (T < 0 || T >= (int64_t(1) << 31) || I <= 0 || I % 8 || T > (int64_t(1) << 40) / I)
+        return MOK_ERROR_INVALID_VALUE;
+    if (T == 0) return MOK_OK;
+    if (!dev_ok(da) || !dev_ok(h) || !dev_ok(dh)) return MOK_ERROR_INVALID_VALUE;
+    const size_t n = (size_t)T * I * 2;
+    if (overlap({dh, 2 * n}, {da, n}) || overlap_partly({dh, 2 * n}, {h, 2 * n})) return MOK_ERROR_INVALID_VALUE;
+    (void)hipGetLastError();
+    return launch_glu_backward(static_cast<const uint16_t *>(da), static_cast<const uint16_t *>(h), T, I,
+                               static_cast<uint16_t *>(dh), static_cast<hipStream_t>(stream));
+}
+
+mok_status mok_fp8_matmul_size(const mok_fp8_shape *shape, size_t *workspace_bytes) {
+    BlkPlan p;
+    const mok_status s = make_blk_matmul_plan(shape, &p);
+    if (s != MOK_OK) return s;
+    if (!workspace_bytes) return MOK_ERROR_INVALID_VALUE;
+    *workspace_bytes = p.total;
+    return MOK_OK;
+}
+
+mok_status mok_fp8_wgrad_size(const mok_fp8_shape *shape, size_t *workspace_bytes) {
+    BlkPlan p;
+    const mok_status s = make_blk_wgrad_plan(shape, &p);
+    if (s != MOK_OK) return s;
+    if (!workspace_bytes) return MOK_ERROR_INVALID_VALUE;
+    *workspace_bytes = p.total;
+    return MOK_OK;
+}
+
+mok_status mok_fp8_matmul(const mok_fp8_shape *shape, void *workspace, size_t workspace_bytes,
+                          const uint8_t *a_elems, const float *a_scales, const uint8_t *b_elems,
+                          const float *b_scales, const int32_t *offsets, void *out, void *stream) {
+    BlkPlan p;
+    const mok_status s = make_blk_matmul_plan(shape, &p);
+    if (s != MOK_OK) return s;
+    if (!dev_ok(workspace) || !dev_ok(b_elems) || !dev_ok(b_scales) || (p.E > 0 ? !dev_ok(offsets) : offsets != nullptr))
+        return MOK_ERROR_INVALID_VALUE;
+    if (p.M > 0 && (!dev_ok(a_elems) || !dev_ok(a_scales) || !dev_ok(out))) return MOK_ERROR_INVALID_VALUE;
+    if (workspace_bytes < p.total) return MOK_ERROR_BUFFER_TOO_SMALL;
+    if (p.M == 0) return MOK_OK;
+    const size_t kb = (size_t)(p.K + 127) / 128, E = (size_t)std::max(p.E, 1);
+    const Span outs[] = {{out, (size_t)p.M * p.N * (p.f32 ? 4 : 2)}, {workspace, p.total}};
+    const Span ins[] = {{a_elems, (size_t)p.M * p.K}, {a_scales, kb * p.M * 4}, {b_elems, E * p.N * p.K},
+                        {b_scales, E * ((p.N + 127) / 128) * kb * 4}, {offsets, ((size_t)p.E + 1) * 4}};
+    if (!apart(outs) || any_overlap(outs[0], ins) || any_overlap(outs[1], ins)) return MOK_ERROR_INVALID_VALUE;
+    (void)hipGetLastError();
+    return launch_fp8_matmul(p, workspace, a_elems, a_scales, b_elems, b_scales, offsets, out,
+                             static_cast<hipStream_t>(stream));
+}
+
+mok_status mok_fp8_wgrad(const mok_fp8_shape *shape, void *workspace, size_t workspace_bytes,
+                         const uint8_t *dy_elems, const float *dy_scales, const uint8_t *x_elems,
+                         const float *x_scales, const int32_t *offsets, const void *addend, void *out, void *stream) {
+    BlkPlan p;
+    const mok_status s = make_blk_wgrad_plan(shape, &p);
+    if (s != MOK_OK) return s;
+    if (!dev_ok(workspace) || !dev_ok(out) || !dev_ok_or_null(addend) ||
+        (p.E > 0 ? !dev_ok(offsets) : offsets != nullptr))
+        return MOK_ERROR_INVALID_VALUE;
+    if (p.M > 0 && (!dev_ok(dy_elems) || !dev_ok(dy_scales) || !dev_ok(x_elems) || !dev_ok(x_scales)))
+        return MOK_ERROR_INVALID_VALUE;
+    if (workspace_bytes < p.total) return MOK_ERROR_BUFFER_TOO_SMALL;
+    const size_t rb = (size_t)(p.M + 127) / 128, n = (size_t)std::max(p.E, 1) * p.N * p.K * (p.f32 ? 4 : 2);
+    const Span outs[] = {{out, n}, {workspace, p.total}}, sadd{addend, n};
+    const Span ins[] = {{dy_elems, (size_t)p.N * p.M}, {dy_scales, rb * p.N * 4}, {x_elems, (size_t)p.K * p.M},
+                        {x_scales, rb * p.K * 4}, {offsets, ((size_t)p.E + 1) * 4}};
+    if (!apart(outs) || any_overlap(outs[0], ins) || any_overlap(outs[1], ins) || overlap_partly(outs[0], sadd) ||
+        overlap(outs[1], sadd))
+        return MOK_ERROR_INVALID_VALUE;
+    (void)hipGetLastError();
+    return launch_fp8_wgrad(p, workspace, dy_elems, dy_scales, x_elems, x_scales, offsets, addend, out,
+                            static_cast<hipStream_t>(stream));
 }
 
 const char *mok_status_string(mok_status status) {

@@ -9,6 +9,7 @@
 #include <atomic>
 
 #include "ffn_plan.h"
+#include "glu.h"
 #include "layer_parts.h"
 #include "mx_codec.h"
 
@@ -289,15 +290,6 @@ __global__ __launch_bounds__(256) void ffn_join_out(const float *__restrict__ pa
     const f32x4_t s = sum_runs(part + idx * 4, (int64_t)T * N, splits);
     reinterpret_cast<uint2 *>(out)[idx] =
         pack4(s[0] + bf16_at(b, 0), s[1] + bf16_at(b, 1), s[2] + bf16_at(b, 2), s[3] + bf16_at(b, 3));
-}
-
-// SwiGLU backward of one value: da arrives, h_g and h_u are the saved rows.
-struct GluGrad {
-    float a, dg, du;
-};
-__device__ __forceinline__ GluGrad glu_backward(float da, float hg, float hu) {
-    const float s = sigmoidf_(hg), sl = hg * s;
-    return GluGrad{sl * hu, da * hu * s * (1.0f + hg * (1.0f - s)), da * sl};
 }
 
 // dh and a from the partials of da = dy W_down^T and the saved h.

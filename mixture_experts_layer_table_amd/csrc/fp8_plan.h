@@ -1,0 +1,21 @@
+// Host-side plan of the products on blocks of 128: tiles and workspace (no HIP calls).
+#pragma once
+#include <cstddef>
+#include <cstdint>
+
+#include "../../include/mok.h"
+
+namespace mok {
+
+struct BlkPlan {
+    int64_t M;
+    int N, K, E;
+    bool f32;
+    int bm;            // tile rows
+    size_t total;      // workspace bytes
+};
+
+mok_status make_blk_matmul_plan(const mok_fp8_shape *s, BlkPlan *p);
+mok_status make_blk_wgrad_plan(const mok_fp8_shape *s, BlkPlan *p);
+
+}  // namespace mok

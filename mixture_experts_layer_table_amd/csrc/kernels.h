@@ -80,6 +80,43 @@ struct NormBackwardCall {
 int64_t norm_backward_shares(int64_t T, int H);
 mok_status launch_add_rmsnorm_backward(const NormBackwardCall &c, hipStream_t st);
 
+// The sort's path: one workgroup (`one`), or `groups` waves of `chunk` slots each.
+struct SortPlan {
+    int64_t n, rows, chunk;
+    int groups;
+    bool one;
+    size_t bytes;   // workspace
+};
+bool sort_plan(int64_t T, int k, int E, int align, SortPlan *p);   // false: a shape outside the limits
+mok_status launch_sort_tokens(const SortPlan &p, int E, int align, const int32_t *ids, void *workspace,
+                              int32_t *offsets, int32_t *slots, int32_t *row_slots, hipStream_t st);
+
+struct RowsCall {
+    int64_t T, rows;
+    int k, E, H;
+    bool f32;
+    const int32_t *offsets, *slots, *row_slots;
+};
+mok_status launch_permute(const RowsCall &c, const void *x, void *rows, uint8_t *elems, float *scales,
+                          hipStream_t st);
+// where: the entry point that the call came through
+mok_status launch_unpermute(const RowsCall &c, const void *y, const float *w, const void *addend, void *out,
+                            const char *where, hipStream_t st);
+mok_status launch_unpermute_backward(const RowsCall &c, const void *dout, const void *y, const float *w, void *dy,
+                                     float *dw, hipStream_t st);
+
+mok_status launch_fp8_quantize(const void *src, bool f32, int64_t batch, int64_t rows, int64_t K, uint32_t flags,
+                               uint8_t *elems, float *scales, hipStream_t st);
+mok_status launch_glu_backward(const uint16_t *da, const uint16_t *h, int64_t T, int I, uint16_t *dh, hipStream_t st);
+
+struct BlkPlan;
+mok_status launch_fp8_matmul(const BlkPlan &p, void *workspace, const uint8_t *a_elems, const float *a_scales,
+                             const uint8_t *b_elems, const float *b_scales, const int32_t *offsets, void *out,
+                             hipStream_t st);
+mok_status launch_fp8_wgrad(const BlkPlan &p, void *workspace, const uint8_t *dy_elems, const float *dy_scales,
+                            const uint8_t *x_elems, const float *x_scales, const int32_t *offsets, const void *addend,
+                            void *out, hipStream_t st);
+
 struct FfnPlan;
 mok_status launch_ffn_forward(const FfnPlan &p, void *workspace, const uint16_t *x, const uint8_t *x_elems,
                               const uint8_t *x_scales, const mok_weights &w, const uint16_t *addend, uint16_t *out,

@@ -1,0 +1,258 @@
+// Token rows sorted by expert and back, and both gradients. With slot[t,j] the
+// row of token t's j-th choice (below 0: none):
+//   permute            rows[slot[t,j]] = x[t]            (as they are, or in 8-bit blocks of 128)
+//   unpermute          out[t] = addend[t] + sum_j w[t,j] y[slot[t,j]]
+//   permute backward   the same sum without weights
+//   unpermute backward dy[slot[t,j]] = w[t,j] dout[t],  dw[t,j] = <dout[t], y[slot[t,j]]>
+// All four go by token: a token's row is read once and stays in registers
+// while its k rows are written (and quantized once, not k times), or its k rows
+// are read into one sum; no row is touched twice and nothing is added through
+// memory. Bound by HBM.
+//
+// Rows that pad an expert's run get zeros from workgroups of their own in the
+// same launch. Slots are checked against the number of rows, so a damaged table
+// can give wrong rows but no access out of range.
+#include "fp8_codec.h"
+#include "kernels.h"
+#include "lanes.h"
+#include "rng.h"
+#include "timing.h"
+
+namespace mok {
+namespace {
+
+constexpr int kRowThreads = 256;            // a chunk of 8 elements each
+constexpr int kPadRows = 32;                // rows that a workgroup looks over for padding, 8 a wave
+constexpr int kBatch = 8;                   // rows in flight per thread
+constexpr int64_t kMostGroups = 1 << 23;    // workgroups of a launch: a grid takes fewer than 2^32 threads
+
+struct RowsArgs {
+    RowsCall c;
+    const void *x, *y, *addend;
+    const float *w;
+    void *rows, *out;
+    uint8_t *elems;
+    float *scales, *dw;
+    int64_t first;       // first workgroup of the launch
+    int64_t tokens_end;  // workgroups below this one take tokens, the others padding
+    int strips;          // workgroups per token
+};
+
+__device__ __forceinline__ bool row_ok(const RowsCall &c, int64_t row) { return (uint64_t)row < (uint64_t)c.rows; }
+
+// Zeros into the padding rows among rows [r0, r0 + 8) of this wave.
+template <Elem E, bool ROWS, bool FP8>
+__device__ __forceinline__ void pad_rows(const RowsArgs &a, int64_t group) {
+    const RowsCall &c = a.c;
+    const int lane = (int)(threadIdx.x & 63), nc = c.H / 8;
+    const int64_t r0 = group * kPadRows + (threadIdx.x >> 6) * 8, end = min((int64_t)c.offsets[c.E], c.rows);
+    for (int i = 0; i < 8; ++i) {
+        const int64_t r = r0 + i;
+        if (r >= end) return;
+        if (c.row_slots[r] >= 0) continue;
+        const float zero[8] = {};
+        for (int h = lane; h < nc; h += 64) {
+            if constexpr (ROWS) store8<E>(a.rows, r * nc + h, zero);
+            if constexpr (FP8) reinterpret_cast<uint2 *>(a.elems)[r * nc + h] = make_uint2(0, 0);
+        }
+        if constexpr (FP8)
+            for (int kb = lane; kb < (c.H + kBlk - 1) / kBlk; kb += 64) a.scales[kb * c.rows + r] = kLeastScale;
+    }
+}
+
+template <Elem E, bool ROWS, bool FP8>
+__global__ __launch_bounds__(kRowThreads) void permute_kernel(RowsArgs a) {
+    const RowsCall &c = a.c;
+    const int64_t b = a.first + blockIdx.x;
+    if (b >= a.tokens_end) {
+        pad_rows<E, ROWS, FP8>(a, b - a.tokens_end);
+        return;
+    }
+    const int64_t t = b / a.strips;
+    const int nc = c.H / 8, h = (int)(b % a.strips) * kRowThreads + (int)threadIdx.x;
+    const bool live = h < nc;
+    float v[8] = {};
+    if (live) unpack8(load8<E>(a.x, t * nc + h), v);
+    uint2 q = make_uint2(0, 0);
+    BlkScale bs{};
+    if constexpr (FP8) {   // 16 neighbouring lanes hold a block
+        bs = blk_scale(max16(amax8(v)));
+        q = make_uint2(blk_codes4(bs, v[0], v[1], v[2], v[3]), blk_codes4(bs, v[4], v[5], v[6], v[7]));
+    }
+    if (!live) return;
+    const int32_t *slots = c.slots + t * c.k;
+    for (int j = 0; j < c.k; ++j) {
+        const int64_t r = slots[j];
+        if (!row_ok(c, r)) continue;
+        if constexpr (ROWS) store8<E>(a.rows, r * nc + h, v);
+        if constexpr (FP8) {
+            reinterpret_cast<uint2 *>(a.elems)[r * nc + h] = q;
+            if (h % 16 == 0) a.scales[h / 16 * c.rows + r] = bs.scale;
+        }
+    }
+}
+
+template <Elem E, bool W>
+__global__ __launch_bounds__(kRowThreads) void unpermute_kernel(RowsArgs a) {
+    const RowsCall &c = a.c;
+    const int64_t b = a.first + blockIdx.x, t = b / a.strips;
+    const int nc = c.H / 8, h = (int)(b % a.strips) * kRowThreads + (int)threadIdx.x;
+    if (h >= nc) return;
+    float s[8] = {}, add[8] = {};
+    if (a.addend) unpack8(load8<E>(a.addend, t * nc + h), add);
+    for (int j0 = 0; j0 < c.k; j0 += kBatch) {
+        Raw8<E> raw[kBatch] = {};
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int64_t r = j0 + j < c.k ? c.slots[t * c.k + j0 + j] : -1;
+            if (row_ok(c, r)) raw[j] = load8<E>(a.y, r * nc + h);
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int64_t r = j0 + j < c.k ? c.slots[t * c.k + j0 + j] : -1;
+            if (!row_ok(c, r)) continue;   // nothing, whatever its weight
+            float v[8], w = 1.0f;
+            if constexpr (W) w = a.w[t * c.k + j0 + j];
+            unpack8(raw[j], v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i] = __builtin_fmaf(w, v[i], s[i]);
+        }
+    }
+    if (a.addend) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] += add[i];
+    }
+    store8<E>(a.out, t * nc + h, s);
+}
+
+// One workgroup a token: each thread walks the row in chunks, with the partial
+// dots of up to kBatch choices in registers.
+template <Elem E>
+__global__ __launch_bounds__(kRowThreads) void unpermute_backward_kernel(RowsArgs a) {
+    __shared__ float red[kRowThreads / 64][kBatch];
+    const RowsCall &c = a.c;
+    const int64_t b = a.first + blockIdx.x;
+    if (b >= a.tokens_end) {
+        pad_rows<E, true, false>(a, b - a.tokens_end);
+        return;
+    }
+    const int64_t t = b;
+    const int nc = c.H / 8, tid = (int)threadIdx.x, wave = tid >> 6;
+    for (int j0 = 0; j0 < c.k; j0 += kBatch) {
+        float dot[kBatch] = {};
+        for (int h = tid; h < nc; h += kRowThreads) {
+            const Raw8<E> dr = load8<E>(a.x, t * nc + h);
+            Raw8<E> yr[kBatch] = {};
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int64_t r = j0 + j < c.k ? c.slots[t * c.k + j0 + j] : -1;
+                if (row_ok(c, r)) yr[j] = load8<E>(a.y, r * nc + h);
+            }
+            float d[8];
+            unpack8(dr, d);
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int64_t r = j0 + j < c.k ? c.slots[t * c.k + j0 + j] : -1;
+                if (!row_ok(c, r)) continue;
+                const float w = a.w[t * c.k + j0 + j];
+                float v[8], g[8];
+                unpack8(yr[j], v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    dot[j] = __builtin_fmaf(d[i], v[i], dot[j]);
+                    g[i] = w * d[i];
+                }
+                store8<E>(a.rows, r * nc + h, g);   // y's own chunk may lie here: read above, by this thread alone
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const float s = sum_wave(dot[j]);
+            if ((tid & 63) == 0) red[wave][j] = s;
+        }
+        __syncthreads();
+        if (tid < kBatch && j0 + tid < c.k) {
+            float s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kRowThreads / 64; ++w) s += red[w][tid];
+            a.dw[t * c.k + j0 + tid] = row_ok(c, c.slots[t * c.k + j0 + tid]) ? s : 0.0f;
+        }
+        __syncthreads();
+    }
+}
+
+template <class K>
+hipError_t launch_groups(K kernel, const char *name, RowsArgs a, int64_t groups, hipStream_t st) {
+    KernelTimer tm(name, st);
+    for (a.first = 0; a.first < groups; a.first += kMostGroups) {
+        const int64_t n = groups - a.first < kMostGroups ? groups - a.first : kMostGroups;
+        kernel<<<(unsigned)n, kRowThreads, 0, st>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+int64_t ceil_of(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace
+
+mok_status launch_permute(const RowsCall &c, const void *x, void *rows, uint8_t *elems, float *scales,
+                          hipStream_t st) {
+    RowsArgs a{};
+    a.c = c;
+    a.x = x;
+    a.rows = rows;
+    a.elems = elems;
+    a.scales = scales;
+    a.strips = (int)ceil_of(c.H / 8, kRowThreads);
+    a.tokens_end = c.T * a.strips;
+    const int64_t groups = a.tokens_end + ceil_of(c.rows, kPadRows);
+    hipError_t e;
+    if (c.f32)
+        e = !elems ? launch_groups(permute_kernel<kF32, true, false>, "permute", a, groups, st)
+            : rows ? launch_groups(permute_kernel<kF32, true, true>, "permute", a, groups, st)
+                   : launch_groups(permute_kernel<kF32, false, true>, "permute", a, groups, st);
+    else
+        e = !elems ? launch_groups(permute_kernel<kBf16, true, false>, "permute", a, groups, st)
+            : rows ? launch_groups(permute_kernel<kBf16, true, true>, "permute", a, groups, st)
+                   : launch_groups(permute_kernel<kBf16, false, true>, "permute", a, groups, st);
+    return check_hip(e, "mok_permute");
+}
+
+mok_status launch_unpermute(const RowsCall &c, const void *y, const float *w, const void *addend, void *out,
+                            const char *where, hipStream_t st) {
+    RowsArgs a{};
+    a.c = c;
+    a.y = y;
+    a.w = w;
+    a.addend = addend;
+    a.out = out;
+    a.strips = (int)ceil_of(c.H / 8, kRowThreads);
+    const int64_t groups = c.T * a.strips;
+    const char *name = "unpermute";
+    const hipError_t e = c.f32 ? (w ? launch_groups(unpermute_kernel<kF32, true>, name, a, groups, st)
+                                    : launch_groups(unpermute_kernel<kF32, false>, name, a, groups, st))
+                               : (w ? launch_groups(unpermute_kernel<kBf16, true>, name, a, groups, st)
+                                    : launch_groups(unpermute_kernel<kBf16, false>, name, a, groups, st));
+    return check_hip(e, where);
+}
+
+mok_status launch_unpermute_backward(const RowsCall &c, const void *dout, const void *y, const float *w, void *dy,
+                                     float *dw, hipStream_t st) {
+    RowsArgs a{};
+    a.c = c;
+    a.x = dout;
+    a.y = y;
+    a.w = w;
+    a.rows = dy;
+    a.dw = dw;
+    a.strips = 1;
+    a.tokens_end = c.T;
+    const int64_t groups = c.T + ceil_of(c.rows, kPadRows);
+    const hipError_t e = c.f32 ? launch_groups(unpermute_backward_kernel<kF32>, "unpermute_backward", a, groups, st)
+                               : launch_groups(unpermute_backward_kernel<kBf16>, "unpermute_backward", a, groups, st);
+    return check_hip(e, "mok_unpermute_backward");
+}
+
+}  // namespace mok
