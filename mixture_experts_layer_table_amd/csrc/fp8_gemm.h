@@ -23,7 +23,7 @@ namespace mok {
 typedef int i32x8v_t __attribute__((ext_vector_type(8)));
 typedef int i32x4v_t __attribute__((ext_vector_type(4)));
 
-template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int NSTAGE_>
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int NSTAGE_, int PER_TILE_, bool EARLY_W_ = false>
 struct BlkCfg {
     static constexpr int BM = BM_, BN = BN_, BK = kBlk;
     static constexpr int WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
@@ -32,46 +32,53 @@ struct BlkCfg {
     static constexpr int FM = WM / 32, FN = WN / 32;
     static constexpr int NSTAGE = NSTAGE_;
     static constexpr int X_BYTES = BM * BK, W_BYTES = BN * BK, STAGE_BYTES = X_BYTES + W_BYTES;
-    static constexpr int SC_OFF = NSTAGE * STAGE_BYTES;   // W row scales, one float per tile row and stage
-    static constexpr size_t LDS_BYTES = (size_t)SC_OFF + (size_t)NSTAGE * BN * 4;
+    // Scales of one stage: 64 floats from each wave (X rows from the first waves, W rows from the last ones). Their
+    // ring is one deeper: those of a block's last tiles are read when its buffer is already being filled.
+    static constexpr int SC_BYTES = NW * 256, SC_W = (NW - BN / 64) * 256;
+    static constexpr int SC_OFF = NSTAGE * STAGE_BYTES;
+    static constexpr size_t LDS_BYTES = (size_t)SC_OFF + (size_t)(NSTAGE + 1) * SC_BYTES;
     static_assert(WM % 32 == 0 && WN == 64, "a wave stores 64 columns");
-    static_assert(BN % 128 == 0 && BN / 64 <= NW, "a wave loads the scales of 64 W rows");
+    static_assert(BM % 128 == 0 && BN % 128 == 0 && BM / 64 + BN / 64 <= NW, "a wave loads 64 rows' scales");
+    // Vector-memory loads of a wave and K-block, and how many it issues per tile (see blk_tile)
+    static constexpr int LOADS = BM / 8 / NW + BN / 8 / NW + 1, PER_TILE = PER_TILE_;
+    static constexpr bool EARLY_W = EARLY_W_;
+    static_assert(NSTAGE >= 2 && LDS_BYTES <= 160 * 1024, "two stages at least; LDS of a compute unit");
 };
 
-// Rows of 128-byte K-blocks into an LDS tile: 8 rows an instruction.
+// Rows of 128-byte K-blocks into an LDS tile: 8 rows an instruction. Lane l of
+// instruction i brings 16 bytes of row 8 i + l / 8 to place l % 8 of it, so it
+// loads chunk (l % 8) ^ ((row >> 1) & 7): the chunks of even and of odd i differ in
+// bit 2 alone. One register a lane holds its offset, one its even chunk.
 template <class C, int ROWS>
 struct BlkLoader {
     static constexpr int IPW = ROWS / 8 / C::NW;
     static_assert(IPW >= 2 && IPW % 2 == 0 && ROWS % (16 * C::NW) == 0, "pairs of instructions per wave");
     rsrc_t res;
-    uint32_t v[2];      // the lane's offset in even and in odd groups of 8 rows (their chunk orders differ)
     uint32_t ld8, lds0;
-    int len, chunk[2];  // bytes of a row's run; the lane's chunk, in bytes
+    int len;            // bytes of a row's run
 
+    static __device__ __forceinline__ uint32_t lane_chunk() {   // in bytes
+        const int L = threadIdx.x & 63;
+        return (uint32_t)(((L & 7) ^ (L >> 4)) * 16);
+    }
+    // The lane's offset from the tile's first row, without its chunk.
+    static __device__ __forceinline__ uint32_t lane_row(uint32_t ld) {
+        return (uint32_t)(wave_id() * IPW * 8 + (int)((threadIdx.x & 63) >> 3)) * ld;
+    }
     // base: the tile's first row at the run's first byte; ld: bytes from row to row
     __device__ __forceinline__ void init(const uint8_t *base, uint32_t ld, int nrows, int len_) {
         len = len_;
         res = make_rsrc(base, nrows > 0 && len > 0 ? (uint32_t)(nrows - 1) * ld + (uint32_t)len : 0u);
-        const int wave = wave_id(), L = threadIdx.x & 63;
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            chunk[p] = ((L & 7) ^ ((p * 4 + (L >> 4)) & 7)) * 16;   // (row >> 1) & 7 of row 8 i + L / 8, i of parity p
-            v[p] = (uint32_t)(wave * IPW * 8 + (L >> 3)) * ld + (uint32_t)chunk[p];
-        }
         ld8 = ld * 8;
-        lds0 = (uint32_t)(wave * IPW * 1024);
+        lds0 = (uint32_t)(wave_id() * IPW * 1024);
     }
-    __device__ __forceinline__ void issue(int kt, uint32_t tile) const {
+    // Instruction i of block kt. Without a branch: what lies behind the run's end (or is a block past the last) is
+    // another row's, so its lanes read zeros instead.
+    __device__ __forceinline__ void issue(int i, int kt, uint32_t tile, uint32_t row, uint32_t chunk) const {
         const int k0 = kt * kBlk;
-        uint32_t o[2] = {v[0], v[1]};
-        if (__builtin_expect(k0 + kBlk > len, 0)) {   // what lies behind the run's end is another row's: zeros instead
-            asm volatile("");
-#pragma unroll
-            for (int p = 0; p < 2; ++p) o[p] = k0 + chunk[p] < len ? v[p] : kOutOfRange;
-        }
-#pragma unroll
-        for (int i = 0; i < IPW; ++i)
-            load_lds16(res, o[i & 1], (uint32_t)k0 + (uint32_t)i * ld8, tile + lds0 + (uint32_t)(i * 1024));
+        const uint32_t c = i % 2 ? chunk ^ 64u : chunk;
+        load_lds16(res, k0 + (int)c < len ? row + c : kOutOfRange, (uint32_t)k0 + (uint32_t)i * ld8,
+                   tile + lds0 + (uint32_t)(i * 1024));
     }
 };
 
@@ -81,24 +88,21 @@ struct BlkLoader {
 struct BlkFrag {
     i32x8v_t h[2];
 };
-struct FragAt {       // the lane's four chunk offsets inside 32 rows
-    uint32_t o[4];
-    __device__ __forceinline__ void init() {
-        const int l = threadIdx.x & 63, r = l & 31;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = (i >> 1) * 4 + (l >> 5) * 2 + (i & 1);
-            o[i] = (uint32_t)(r * kBlk + ((c ^ ((r >> 1) & 7)) << 4));
-        }
-    }
-};
-__device__ __forceinline__ BlkFrag read_frag(const FragAt &at, uint32_t tile) {
+// The lane's first chunk inside 32 rows; the others lie at it ^ 16 (the next chunk), ^ 64 (the other half) and ^ 80.
+__device__ __forceinline__ uint32_t frag_lane() {
+    const int l = threadIdx.x & 63, r = l & 31;
+    return (uint32_t)(r * kBlk + (((l >> 5) * 2) ^ ((r >> 1) & 7)) * 16);
+}
+// Fragment at `at` (a multiple of 128 bytes, and frag_lane() added) + OFF, a constant that goes into the instructions.
+template <uint32_t OFF>
+__device__ __forceinline__ BlkFrag read_frag(uint32_t at) {
     typedef __attribute__((address_space(3))) i32x4v_t lds4_t;
+    typedef __attribute__((address_space(3))) char lds_t;
     BlkFrag f;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        const i32x4v_t lo = *(const lds4_t *)(uintptr_t)(tile + at.o[2 * s]);
-        const i32x4v_t hi = *(const lds4_t *)(uintptr_t)(tile + at.o[2 * s + 1]);
+        const i32x4v_t lo = *(const lds4_t *)((const lds_t *)(uintptr_t)(at ^ (uint32_t)(64 * s)) + OFF);
+        const i32x4v_t hi = *(const lds4_t *)((const lds_t *)(uintptr_t)(at ^ (uint32_t)(64 * s + 16)) + OFF);
         f.h[s] = i32x8v_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     }
     return f;

@@ -9,8 +9,8 @@
 namespace mok {
 namespace {
 
-using CfgL = BlkCfg<256, 256, 2, 4, 2>;
-using CfgM = BlkCfg<128, 256, 2, 4, 2>;
+using CfgL = BlkCfg<256, 256, 2, 4, 2, 3, true>;
+using CfgM = BlkCfg<128, 256, 2, 4, 3, 3>;
 
 struct BlkArgs {
     int64_t xs_ld, ws_ld;    // entries from one block's scales to the next (X; W by rows)
@@ -20,7 +20,7 @@ struct BlkArgs {
     const void *addend;
     void *out;
     int M, N, K, E;          // output rows (of all experts together, or of one), columns, contraction
-    int ldx, ldw;            // bytes from row to row
+    int ld;                  // bytes from row to row, of both
 };
 
 // One tile: output rows [m0, m0 + rows) x columns [n0, ..), contraction [k0, k0 + len).
@@ -101,11 +101,40 @@ __device__ __forceinline__ bool locate(const BlkArgs &a, int bm, int n_tiles, in
 
 // ----------------------------------------------------------------------------- the tile's product
 
+// x of lane R of the lane's row of 16
+template <int R>
+__device__ __forceinline__ float lane_of_16(float x) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x150 + R, 0xF, 0xF, true));
+}
+
+// acc += p * s, or with a scale per W row (register R's in lane R of 16) acc += p * (s * sw_R)
+template <bool WROWS, int... R>
+__device__ __forceinline__ void scaled_add(f32x16_t &acc, const f32x16_t &p, float s, float sw,
+                                           std::integer_sequence<int, R...>) {
+    ((acc[R] = __builtin_fmaf(p[R], WROWS ? s * lane_of_16<R>(sw) : s, acc[R])), ...);
+}
+
 // WROWS: W has a scale per row and block (weight gradients), else per 128 rows and
 // block. F32: fp32 results, whose products are exact (blk_product).
+//
+// A wave goes through its FM x FN block tiles of a K-block in row order, one
+// tile's MFMAs issued ahead of the previous tile's multiply-adds (two product
+// registers in turn), so that the matrix cores run through. X fragments are read
+// one row of tiles ahead. One barrier a K-block, ahead of its last row of tiles:
+// by then every fragment of block kt is in registers, so its buffer can take block
+// kt + NSTAGE; and block kt + 1 has landed, whose first fragments are read during
+// that last row. Loads thus have (NSTAGE - 1) K-blocks' time. With two stages
+// (EARLY_W) that is short, so a second barrier after the first row frees the W half
+// of the buffer, whose fragments a wave holds through the block: its loads go out
+// half a block sooner.
+// 16,384 x 4,096 x 7,168 on one card: 581 us as a plain loop, 432 with products in
+// turn, 401 with the loads in branchless form, 386 with three of a wave's nine loads
+// a tile instead of all behind the barrier, 371 with the second barrier; 282 without
+// loads and multiply-adds, where the clock (1.9 GHz) is the limit.
 template <class C, bool WROWS, bool F32>
 __device__ __forceinline__ void blk_tile(const BlkArgs &a, const BlkTile &t, uint32_t lds) {
-    constexpr int FM = C::FM, FN = C::FN;
+    constexpr int FM = C::FM, FN = C::FN, S = C::NSTAGE;
+    static_assert(FN == 2 && FM >= 2, "two products in turn; fragments one row of tiles ahead");
     const int wave = wave_id(), wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
     const int lane = threadIdx.x & 63;
     const int nk = uniform_i((t.len + kBlk - 1) / kBlk);
@@ -119,88 +148,144 @@ __device__ __forceinline__ void blk_tile(const BlkArgs &a, const BlkTile &t, uin
 
     BlkLoader<C, C::BM> xl;
     BlkLoader<C, C::BN> wl;
-    xl.init(t.x, (uint32_t)a.ldx, t.rows, t.len);
-    wl.init(t.w, (uint32_t)a.ldw, t.cols, t.len);
-    FragAt at;
-    at.init();
-    const uint32_t xs_off = (uint32_t)(wm * C::WM + (lane & 31)) * 4u;
-    const float *ws_tile = t.ws;   // scales of the wave's 128 W rows, one per block
-    if constexpr (!WROWS) ws_tile += (int64_t)min(wn * 64 / kBlk, (t.cols - 1) / kBlk) * a.ws_ld;
+    xl.init(t.x, (uint32_t)a.ld, t.rows, t.len);
+    wl.init(t.w, (uint32_t)a.ld, t.cols, t.len);
+    const uint32_t chunk = xl.lane_chunk(), x_row = xl.lane_row((uint32_t)a.ld);
+    const uint32_t w_row = C::BM == C::BN ? x_row : wl.lane_row((uint32_t)a.ld);
+    constexpr int L = C::LOADS, XL = BlkLoader<C, C::BM>::IPW;
+    const uint32_t frag = frag_lane();
+    // This wave's scales of a K-block: those of 64 rows of X, or of 64 rows of W where each has its own; else the last
+    // wave brings those of the tile's 128-row blocks of W, and the others none (zeros land in their places).
+    const bool x_scales = wave < C::BM / 64, w_scales = WROWS ? wave * 256 >= C::SC_W : wave == C::NW - 1;
+    const int sc_row = x_scales ? wave * 64 : WROWS ? wave * 64 - C::SC_W / 4 : 0;
+    const float *sc_src = x_scales ? t.xs + sc_row : t.ws + sc_row;
+    const int64_t sc_ld = x_scales ? a.xs_ld : WROWS ? a.ws_ld : 1;
+    const int blocks = (t.cols + kBlk - 1) / kBlk;
+    const uint32_t sc_bytes =
+        x_scales   ? (uint32_t)max(t.rows - sc_row, 0) * 4u
+        : w_scales ? WROWS ? (uint32_t)max(t.cols - sc_row, 0) * 4u : (uint32_t)((blocks - 1) * (int)a.ws_ld + 1) * 4u
+                   : 0u;
+    const uint32_t sc_lane = x_scales || WROWS ? 4u : 4u * (uint32_t)a.ws_ld;   // bytes from a lane's scale to the next
 
-    float sx[FM], sx_next[FM], sw_lane = 0.0f;
-    auto stage = [&](int kt) { return lds + (uint32_t)((kt % C::NSTAGE) * C::STAGE_BYTES); };
-    auto w_scales = [&](int kt) { return lds + (uint32_t)(C::SC_OFF + (kt % C::NSTAGE) * C::BN * 4); };
-    auto issue = [&](int kt) {
-        const uint32_t st = stage(kt);
-        xl.issue(kt, st);
-        wl.issue(kt, st + C::X_BYTES);
+    // Ring positions by counters: the compiler would otherwise keep an address register for each read.
+    auto stage = [&](int kt) { return lds + (uint32_t)((kt % S) * C::STAGE_BYTES); };
+    auto scales = [&](int kt) { return lds + (uint32_t)(C::SC_OFF + (kt % (S + 1)) * C::SC_BYTES); };
+    auto issue = [&](int i, int kt, uint32_t st, uint32_t sc) {   // load i of block kt
+        if (i == 0)
+            load_lds4(make_rsrc(sc_src + (int64_t)kt * sc_ld, kt < nk ? sc_bytes : 0u), (uint32_t)lane * sc_lane, 0,
+                      sc + (uint32_t)wave * 256u);
+        else if (i <= XL)
+            xl.issue(i - 1, kt, st, x_row, chunk);
+        else
+            wl.issue(i - 1 - XL, kt, st + C::X_BYTES, w_row, chunk);
+    };
+    // Loads of block kt that go out with tile `at` after the barrier that frees its buffer: PER_TILE each, so that
+    // the waves do not queue for the load path when they all leave the barrier.
+    auto issue_with = [&](int at, int kt, uint32_t st, uint32_t sc) {
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+            if (i / C::PER_TILE == at) issue(i, kt, st, sc);
+    };
+    typedef __attribute__((address_space(3))) float lds_f32;
+    const uint32_t x_rows = (uint32_t)(wm * C::WM * kBlk), w_rows = (uint32_t)(wn * 64 * kBlk);
+    const uint32_t sw_at = (uint32_t)((C::NW - 1) * 256 + min(wn * 64 / kBlk, blocks - 1) * 4);
+    BlkFrag w[FN], x[2];
+    float sx[FM], sw = 1.0f;
+    auto read_sx = [&](uint32_t sc) {
+        if constexpr (!WROWS) sw = *(const lds_f32 *)(uintptr_t)(sc + sw_at);
+        const uint32_t b = sc + (uint32_t)(wm * C::WM + (lane & 31)) * 4u;
+#pragma unroll
+        for (int fm = 0; fm < FM; ++fm) sx[fm] = *((const lds_f32 *)(uintptr_t)b + fm * 32);
+    };
+    f32x16_t p[FN];   // the last one, zero at first, is added a step after the K-block it belongs to
+    // Scales of W rows: lane k of each 16 holds that of the k-th of the lane half's 16 columns of a block tile, and a
+    // multiplication takes it from there for all 16 lanes (row_newbcast); 16 registers of broadcast copies would cost
+    // as much LDS time as the fragments.
+    float sw_rows[FN] = {}, last = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) p[FN - 1][r] = 0.0f;
+    auto join = [&](int fm, int fn) {   // p[fn] into its accumulator; last: the row's scale (times the tile's)
+        asm volatile("" : "+v"(sw_rows[fn]));   // broadcast anew for each tile: kept, the copies would spill
+        scaled_add<WROWS>(acc[fm][fn], p[fn], last, sw_rows[fn], std::make_integer_sequence<int, 16>{});
+        asm volatile("" : "+v"(acc[fm][fn]));   // here, not past the next barrier
+    };
+    auto read_sw = [&](uint32_t sc) {
         if constexpr (WROWS) {
-            if (wave < C::BN / 64)
-                load_lds4(make_rsrc(t.ws + (int64_t)kt * a.ws_ld, (uint32_t)t.cols * 4u),
-                          (uint32_t)(wave * 64 + lane) * 4u, 0, w_scales(kt) + (uint32_t)wave * 256u);
+            const uint32_t b =
+                sc + (uint32_t)(C::SC_W + (wn * 64 + ((lane & 15) >> 2) * 8 + (lane >> 5) * 4 + (lane & 3)) * 4);
+#pragma unroll
+            for (int fn = 0; fn < FN; ++fn) sw_rows[fn] = *((const lds_f32 *)(uintptr_t)b + fn * 32);
         }
     };
-    auto load_sx = [&](int kt, float (&s)[FM]) {
-        const brsrc_t r = rows_rsrc(t.xs + (int64_t)kt * a.xs_ld, (uint32_t)t.rows * 4u);
-#pragma unroll
-        for (int fm = 0; fm < FM; ++fm)
-            s[fm] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (int)(xs_off + (uint32_t)fm * 128u), 0, 0));
-    };
-    if (nk > 0) {
-        issue(0);
-        load_sx(0, sx);
-    }
-    for (int kt = 0; kt < nk; ++kt) {
-        wait_vmcnt<0>();
-#pragma unroll
-        for (int fm = 0; fm < FM; ++fm) asm volatile("" : "+v"(sx[fm]));
-        lds_barrier();   // block kt has landed, and no wave reads block kt - 1 any more
-        if constexpr (!WROWS) {
-            if (kt % 64 == 0) {   // the next 64 blocks' scales, one a lane
-                sw_lane = ws_tile[min(kt + lane, nk - 1)];
-                asm volatile("" : "+v"(sw_lane));
-            }
-        }
-        if (kt + 1 < nk) {
-            issue(kt + 1);
-            load_sx(kt + 1, sx_next);
-        }
-        const uint32_t st = stage(kt);
-        BlkFrag w[FN];
-#pragma unroll
-        for (int fn = 0; fn < FN; ++fn) w[fn] = read_frag(at, st + (uint32_t)(C::X_BYTES + (wn * 64 + fn * 32) * kBlk));
-        float s[FM];
-        if constexpr (!WROWS) {
-            const float sw = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(sw_lane), kt % 64));
-#pragma unroll
-            for (int fm = 0; fm < FM; ++fm) s[fm] = sx[fm] * sw;
-        }
+    // K-block kt
+    auto block = [&](int kt) {
+        uint32_t st = stage(kt), st1 = stage(kt + 1), sc = scales(kt), sc1 = scales(kt + 1);
+        uint32_t stp = stage(kt + S - 1), scp = scales(kt + S - 1), scn = scales(kt + S);
+        asm volatile("" : "+s"(st), "+s"(st1), "+s"(sc), "+s"(sc1), "+s"(stp), "+s"(scp), "+s"(scn));
 #pragma unroll
         for (int fm = 0; fm < FM; ++fm) {
-            const BlkFrag x = read_frag(at, st + (uint32_t)((wm * C::WM + fm * 32) * kBlk));
+            if (fm == FM - 1) {
+                wait_lgkm0();   // the block's last fragments are in registers
+                if constexpr (C::EARLY_W) wait_vmcnt<L - 1 - XL>();
+                else wait_vmcnt<(S - 2) * L>();
+                lds_barrier();
+            }
+            if (C::EARLY_W && fm == 1) {
+                wait_lgkm0();   // W of block kt is in every wave's registers behind this barrier
+                lds_barrier();
+            }
+            const float s = sx[fm] * sw;
 #pragma unroll
             for (int fn = 0; fn < FN; ++fn) {
-                const f32x16_t p = blk_product<F32>(w[fn], x);
-                if constexpr (WROWS) {
-                    const uint32_t sa = w_scales(kt) + (uint32_t)(wn * 64 + fn * 32 + (lane >> 5) * 4) * 4u;
-#pragma unroll
-                    for (int g4 = 0; g4 < 4; ++g4) {
-                        const f32x4_t sw = *(const __attribute__((address_space(3))) f32x4_t *)(uintptr_t)(sa + g4 * 32);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            acc[fm][fn][g4 * 4 + j] =
-                                __builtin_fmaf(p[g4 * 4 + j], sx[fm] * sw[j], acc[fm][fn][g4 * 4 + j]);
-                    }
-                } else {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) acc[fm][fn][r] = __builtin_fmaf(p[r], s[fm], acc[fm][fn][r]);
+                __builtin_amdgcn_sched_barrier(0);
+                if (fn == 0) {
+                    if (fm == 0) x[1] = read_frag<1 * 32 * kBlk>(st + x_rows + frag);
+                    if (fm == 1 && FM > 2) x[0] = read_frag<2 * 32 * kBlk>(st + x_rows + frag);
+                    if (fm == 2) x[1] = read_frag<3 * 32 * kBlk>(st + x_rows + frag);
+                    if (fm == FM - 1) x[0] = read_frag<0>(st1 + x_rows + frag);
                 }
+                p[fn] = blk_product<F32>(w[fn], x[fm & 1]);
+                __builtin_amdgcn_sched_barrier(0);
+                if (fm == FM - 1)
+                    w[fn] = fn == 0 ? read_frag<C::X_BYTES>(st1 + w_rows + frag)
+                                    : read_frag<C::X_BYTES + 32 * kBlk>(st1 + w_rows + frag);
+                if constexpr (C::EARLY_W) {
+#pragma unroll
+                    for (int i = 0; i < L; ++i)
+                        if (i <= XL ? fm == FM - 1 && fn == i / 3 : fm == 1 + (i - 1 - XL) / 4 && fn == (i - 1 - XL) / 2 % 2)
+                            issue(i, kt + S, st, scn);
+                } else if (fm == FM - 1) {
+                    issue_with(fn, kt + S, st, scn);
+                } else {
+                    issue_with(FN + fm * FN + fn, kt + S - 1, stp, scp);
+                }
+                if (fn > 0) join(fm, fn - 1);
+                else join((fm + FM - 1) % FM, FN - 1);
+                if (fm == 0 && fn == 0) read_sw(sc);
+                last = s;
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
-        wait_lgkm0();
+        read_sx(sc1);
+    };
+    // as if block -1 had come before
 #pragma unroll
-        for (int fm = 0; fm < FM; ++fm) sx[fm] = sx_next[fm];
-    }
+    for (int i = 0; i < S - 1; ++i)
+#pragma unroll
+        for (int at = 0; at < FM * FN; ++at) issue_with(at, i, stage(i), scales(i));
+    constexpr int EARLY = C::EARLY_W || 2 * C::PER_TILE >= L ? L : 2 * C::PER_TILE;
+#pragma unroll
+    for (int i = 0; i < EARLY; ++i) issue(i, S - 1, stage(S - 1), scales(S - 1));
+    static_assert((L + C::PER_TILE - 1) / C::PER_TILE <= FM * FN, "a block's loads go out before the next barrier");
+    wait_vmcnt<(S - 2) * L + EARLY>();
+    lds_barrier();
+    read_sx(scales(0));
+    x[0] = read_frag<0>(stage(0) + x_rows + frag);
+    w[0] = read_frag<C::X_BYTES>(stage(0) + w_rows + frag);
+    w[1] = read_frag<C::X_BYTES + 32 * kBlk>(stage(0) + w_rows + frag);
+    for (int kt = 0; kt < nk; ++kt) block(kt);
+    join(FM - 1, FN - 1);
+    wait_vmcnt<0>();   // the loads of blocks past the last, which write zeros
     lds_barrier();   // the waves' staging areas lie where blocks were
 
     // out = addend + acc: rows through the wave's staging area (bf16), or 16 bytes a lane (fp32)
@@ -300,8 +385,8 @@ __global__ __launch_bounds__(C::NT, 2) void blk_wgrad(BlkArgs a) {
         r1 = uniform_i(clamp_row(a.offsets[e + 1], a.K));
     }
     BlkTile t;
-    t.x = a.x + (int64_t)m0 * a.ldx + r0;
-    t.w = a.w + (int64_t)n0 * a.ldw + r0;
+    t.x = a.x + (int64_t)m0 * a.ld + r0;
+    t.w = a.w + (int64_t)n0 * a.ld + r0;
     t.xs = a.xs + (int64_t)(r0 / kBlk) * a.xs_ld + m0;
     t.ws = a.ws + (int64_t)(r0 / kBlk) * a.ws_ld + n0;
     t.rows = min(C::BM, a.M - m0);
@@ -368,7 +453,7 @@ mok_status launch_fp8_matmul(const BlkPlan &p, void *workspace, const uint8_t *a
     a.N = p.N;
     a.K = p.K;
     a.E = p.E;
-    a.ldx = a.ldw = p.K;
+    a.ld = p.K;
     hipError_t e;
     if (p.f32) e = launch_matmul<CfgM, true>(a, st);
     else e = p.bm == CfgM::BM ? launch_matmul<CfgM, false>(a, st) : launch_matmul<CfgL, false>(a, st);
@@ -393,7 +478,7 @@ mok_status launch_fp8_wgrad(const BlkPlan &p, void *workspace, const uint8_t *dy
     a.N = p.K;
     a.K = (int)p.M;
     a.E = p.E;
-    a.ldx = a.ldw = (int)p.M;
+    a.ld = (int)p.M;
     hipError_t e;
     if (p.f32) e = launch_wgrad<CfgM, true>(a, st);
     else e = p.bm == CfgM::BM ? launch_wgrad<CfgM, false>(a, st) : launch_wgrad<CfgL, false>(a, st);
