@@ -2,9 +2,8 @@
 // grouped by expert, and the weight gradients.
 #include <atomic>
 
-#include "fp8_gemm.h"
 #include "fp8_plan.h"
-#include "layer_parts.h"
+#include "fp8_tiles.h"
 
 namespace mok {
 namespace {
@@ -12,94 +11,181 @@ namespace {
 using CfgL = BlkCfg<256, 256, 2, 4, 2, 3, true>;
 using CfgM = BlkCfg<128, 256, 2, 4, 3, 3>;
 
-struct BlkArgs {
-    int64_t xs_ld, ws_ld;    // entries from one block's scales to the next (X; W by rows)
-    const uint8_t *x, *w;
-    const float *xs, *ws;
-    const int32_t *offsets;  // NULL: one product
-    const void *addend;
-    void *out;
-    int M, N, K, E;          // output rows (of all experts together, or of one), columns, contraction
-    int ld;                  // bytes from row to row, of both
-};
-
 // One tile: output rows [m0, m0 + rows) x columns [n0, ..), contraction [k0, k0 + len).
 struct BlkTile {
     const uint8_t *x, *w;    // first row at k0
     const float *xs, *ws;    // scales of the first row (W by tiles: the first block row) at k0
     int rows, cols, len;
-    int64_t out;             // first element in out
+    int64_t out;             // first element in out (and in a run's partials)
+    float *part;             // partials of the tile's run of the contraction
 };
-
-__device__ __forceinline__ int clamp_row(int v, int M) { return min(max(v, 0), M); }
 
 // ----------------------------------------------------------------------------- tiles
 
-// Number of row tiles of expert e (lane-wise), its first row and its rows.
-__device__ __forceinline__ int expert_tiles(const BlkArgs &a, int bm, int e, int &lo, int &n) {
-    lo = n = 0;
-    if (e < a.E) {
-        lo = clamp_row(a.offsets[e], a.M);
-        n = max(clamp_row(a.offsets[e + 1], a.M) - lo, 0);
-    }
-    return (n + bm - 1) / bm;
+// Workgroup b of a segment of 8 * per workgroups -> tile; each XCD walks a contiguous range.
+__device__ __forceinline__ int xcd_tile(int b, int per) { return (b % kXcds) * per + b / kXcds; }
+// Tile id of total x cols in groups of kGroupM row tiles x all columns -> (row tile, column).
+__device__ __forceinline__ void group_tile(int id, int total, int cols, int &mt, int &col) {
+    const int gsize = kGroupM * cols, first = id / gsize * kGroupM, gm = min(kGroupM, total - first), r = id % gsize;
+    mt = first + r % gm;
+    col = r / gm;
 }
-__device__ __forceinline__ int lane_scan(int v) {   // inclusive
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(v, d);
-        if ((int)(threadIdx.x & 63) >= d) v += o;
-    }
-    return v;
-}
-__device__ __forceinline__ int uniform_i(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// Row tile and column tile of workgroup b; false: none. As in the segment GEMMs
-// each XCD walks a contiguous range of tiles, in groups of kGroupM row tiles.
 struct RowTile {
-    int e, m0, rows, nt;
+    int e, m0, rows, nt, s;   // s: run of the contraction
 };
-__device__ __forceinline__ bool locate(const BlkArgs &a, int bm, int n_tiles, int b, RowTile &t) {
-    int total = (a.M + bm - 1) / bm;
-    const int lane = threadIdx.x & 63;
-    if (a.E > 0) {
-        total = 0;
-        for (int e0 = 0; e0 < a.E; e0 += 64) {
-            int lo, n;
-            total += __shfl(lane_scan(expert_tiles(a, bm, e0 + lane, lo, n)), 63);
-        }
-        total = uniform_i(total);
-    }
-    const int all = total * n_tiles, per = (all + kXcds - 1) / kXcds, id = (b % kXcds) * per + b / kXcds;
+// Workgroup b of tiles of bm rows, every one cut into `splits` runs; false: none.
+__device__ __forceinline__ bool locate(const BlkArgs &a, int bm, int n_tiles, int splits, int b, RowTile &t) {
+    const auto tiles = [bm](int n) { return (n + bm - 1) / bm; };
+    const int total = count_tiles(a, tiles), cols = n_tiles * splits, all = total * cols;
+    const int per = (all + kXcds - 1) / kXcds, id = xcd_tile(b, per);
     if (b / kXcds >= per || id >= all) return false;
-    const int gsize = kGroupM * n_tiles, first = id / gsize * kGroupM, gm = min(kGroupM, total - first), r = id % gsize;
-    const int mt = first + r % gm;
-    t.nt = r / gm;
-    if (a.E == 0) {
-        t.e = 0;
-        t.m0 = mt * bm;
-        t.rows = min(bm, a.M - t.m0);
+    int mt, col;
+    group_tile(id, total, cols, mt, col);
+    t.nt = col % n_tiles;
+    t.s = col / n_tiles;
+    const Found f = find_tile(a, mt, tiles);
+    t.e = f.e;
+    t.m0 = f.lo + f.i * bm;
+    t.rows = min(bm, f.n - f.i * bm);
+    return true;
+}
+
+// Workgroup b of tiles of 256 rows and of 128 (half), which take 0.6 of their time:
+// an expert's last rows go to a half tile if they fit, and where the whole tiles
+// end in a round of at most kUnits / 2, that round takes them as halves. false: none.
+constexpr int kUnits = 256;   // compute units
+__device__ __forceinline__ bool locate_mixed(const BlkArgs &a, int n_tiles, int b, RowTile &t, bool &half) {
+    const auto whole = [](int n) { return n / 256 + (n % 256 > 128); };
+    const auto rest = [](int n) { return n % 256 > 0 && n % 256 <= 128 ? 1 : 0; };
+    const int wholes = count_tiles(a, whole), rests = count_tiles(a, rest);
+    int full = wholes * n_tiles, halves = full % kUnits;
+    if (halves <= kUnits / 2) full -= halves;
+    else halves = 0;
+    const int all[3] = {full, 2 * halves, rests * n_tiles};
+    int seg = 0, id = 0;
+    for (; seg < 3; ++seg) {
+        const int per = (all[seg] + kXcds - 1) / kXcds;
+        id = xcd_tile(b, per);
+        if (b < per * kXcds) break;
+        b -= per * kXcds;
+    }
+    if (seg == 3 || id >= all[seg]) return false;
+    t.s = 0;
+    half = seg > 0;
+    int mt;
+    if (seg == 2) {
+        group_tile(id, rests, n_tiles, mt, t.nt);
+        const Found f = find_tile(a, mt, rest);
+        t.e = f.e;
+        t.m0 = f.lo + f.n / 256 * 256;
+        t.rows = f.n % 256;
         return true;
     }
-    int before = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 64) {
-        int lo, n;
-        const int c = expert_tiles(a, bm, e0 + lane, lo, n), incl = before + lane_scan(c);
-        const uint64_t past = __ballot(incl > mt);
-        if (past) {
-            const int who = __builtin_ctzll(past);
-            const int i = mt - __shfl(incl - c, who);
-            t.e = uniform_i(e0 + who);
-            t.m0 = uniform_i(__shfl(lo, who) + i * bm);
-            t.rows = uniform_i(min(bm, __shfl(n, who) - i * bm));
-            return true;
-        }
-        before = __shfl(incl, 63);
-    }
-    return false;
+    group_tile(seg == 0 ? id : full + id / 2, wholes, n_tiles, mt, t.nt);
+    const Found f = find_tile(a, mt, whole);
+    const int below = f.i * 256 + (half ? id % 2 * 128 : 0);
+    t.e = f.e;
+    t.m0 = f.lo + below;
+    t.rows = min(half ? 128 : 256, f.n - below);
+    return true;
 }
 
 // ----------------------------------------------------------------------------- the tile's product
+
+typedef uint32_t u32x4s_t __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void put16(uint32_t a, f32x4_t v) {
+    *reinterpret_cast<__attribute__((address_space(3))) f32x4_t *>((uintptr_t)a) = v;
+}
+__device__ __forceinline__ f32x4_t get16(uint32_t a) {
+    return *reinterpret_cast<const __attribute__((address_space(3))) f32x4_t *>((uintptr_t)a);
+}
+
+// out = addend + acc for the wave's 64 columns of a tile, N columns a row, rounded
+// once. 32 rows at a time pass through the wave's own part of the LDS (whose
+// accesses complete in order), so that stores and the addend's loads take whole
+// runs of a row: a lane's accumulators hold 4 columns of one row. Staged as fp32
+// rows of 256 bytes where an addend has to be added first, else as they are stored.
+// 16-byte unit u of row r lies at u ^ (r % 16), in bf16 rows at u ^ (r / 2 % 8).
+template <class C, bool F32>
+__device__ __forceinline__ void store_tile(const f32x16_t (&acc)[C::FM][C::FN], const BlkTile &t, int N, void *out,
+                                           const void *addend, uint32_t lds, int wm, int wn) {
+    constexpr int FM = C::FM, FN = C::FN;
+    static_assert(C::NW * 8192 <= C::LDS_BYTES, "8 KiB a wave");
+    const int c0 = wn * 64, el = epi_lane(), row = el & 31, half = el >> 5;
+    const int valid = min(t.cols - c0, 64);   // a multiple of 16
+    constexpr uint32_t es = F32 ? 4u : 2u;
+    const uint32_t row_bytes = (uint32_t)N * es;
+    const uint32_t bytes = valid > 0 ? (uint32_t)(t.rows - 1) * row_bytes + (uint32_t)valid * es : 0u;
+    const int64_t at_byte = (valid > 0 ? t.out + c0 : 0) * es;
+    const brsrc_t dst = rows_rsrc(static_cast<char *>(out) + at_byte, bytes);
+    const uint32_t area = lds + (uint32_t)wave_id() * 8192u;
+    if (F32 || addend) {
+        const brsrc_t add = rows_rsrc(addend ? static_cast<const char *>(addend) + at_byte : static_cast<char *>(out),
+                                      addend ? bytes : 0u);
+        const int pr = el >> 4, pu = el & 15;   // a pass: 4 rows of 16 lanes, 4 columns each
+        const uint32_t v0 = pu * 4 < valid ? (uint32_t)(wm * C::WM + pr) * row_bytes + (uint32_t)pu * 4u * es : kOutOfRange;
+#pragma unroll
+        for (int fm = 0; fm < FM; ++fm) {
+#pragma unroll
+            for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+                for (int g4 = 0; g4 < 4; ++g4) {
+                    const uint32_t u = (uint32_t)(fn * 8 + g4 * 2 + half);
+                    const f32x16_t &c = acc[fm][fn];
+                    put16(area + (uint32_t)row * 256u + ((u ^ (uint32_t)(row & 15)) << 4),
+                          f32x4_t{c[g4 * 4], c[g4 * 4 + 1], c[g4 * 4 + 2], c[g4 * 4 + 3]});
+                }
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+                const int r = p * 4 + pr;
+                const uint32_t v = v0 + (uint32_t)(fm * 32 + p * 4) * row_bytes;
+                f32x4_t y = get16(area + (uint32_t)r * 256u + (uint32_t)((pu ^ (r & 15)) << 4));
+                if constexpr (F32) {
+                    if (addend) {
+                        const u32x4s_t b = __builtin_amdgcn_raw_buffer_load_b128(add, (int)v, 0, 0);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) y[j] += __uint_as_float(b[j]);
+                    }
+                    const u32x4s_t w = {__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]),
+                                        __float_as_uint(y[3])};
+                    __builtin_amdgcn_raw_buffer_store_b128(w, dst, (int)v, 0, 0);
+                } else {
+                    const uint2 b = bload8(add, v, 0);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) y[j] += bf16_at(b, j);
+                    bstore8_nt(dst, v, 0, make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])));
+                }
+            }
+        }
+    } else {
+        const int pr = el >> 3, pu = el & 7;    // a pass: 8 rows of 8 lanes, 8 columns each
+        const uint32_t v0 = pu * 8 < valid ? (uint32_t)(wm * C::WM + pr) * row_bytes + (uint32_t)pu * 16u : kOutOfRange;
+#pragma unroll
+        for (int fm = 0; fm < FM; ++fm) {
+#pragma unroll
+            for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+                for (int g4 = 0; g4 < 4; ++g4) {
+                    const f32x16_t &c = acc[fm][fn];
+                    const uint32_t u = (uint32_t)(fn * 4 + g4);
+                    u32x2v_t w;
+                    w.x = pack_bf16x2(c[g4 * 4], c[g4 * 4 + 1]);
+                    w.y = pack_bf16x2(c[g4 * 4 + 2], c[g4 * 4 + 3]);
+                    *reinterpret_cast<__attribute__((address_space(3))) u32x2v_t *>(
+                        (uintptr_t)(area + (uint32_t)row * 128u + ((u ^ (uint32_t)(row >> 1 & 7)) << 4) + (uint32_t)half * 8u)) = w;
+                }
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const int r = p * 8 + pr;
+                const f32x4_t y = get16(area + (uint32_t)r * 128u + (uint32_t)((pu ^ (r >> 1 & 7)) << 4));
+                const u32x4s_t w = {__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]),
+                                    __float_as_uint(y[3])};
+                __builtin_amdgcn_raw_buffer_store_b128(w, dst, (int)(v0 + (uint32_t)(fm * 32 + p * 8) * row_bytes), 0, 2);
+            }
+        }
+    }
+}
 
 // x of lane R of the lane's row of 16
 template <int R>
@@ -288,101 +374,67 @@ __device__ __forceinline__ void blk_tile(const BlkArgs &a, const BlkTile &t, uin
     wait_vmcnt<0>();   // the loads of blocks past the last, which write zeros
     lds_barrier();   // the waves' staging areas lie where blocks were
 
-    // out = addend + acc: rows through the wave's staging area (bf16), or 16 bytes a lane (fp32)
-    const int c0 = wn * 64, el = epi_lane();
-    const int valid = min(t.cols - c0, 64);   // a multiple of 16
-    constexpr uint32_t es = F32 ? 4u : 2u;
-    const uint32_t row_bytes = (uint32_t)a.N * es;
-    const int64_t o = t.out + c0;
-    const uint32_t bytes = valid > 0 ? (uint32_t)(t.rows - 1) * row_bytes + (uint32_t)valid * es : 0u;
-    const int64_t at_byte = (valid > 0 ? o : 0) * es;
-    const brsrc_t dst = rows_rsrc(static_cast<char *>(a.out) + at_byte, bytes);
-    const brsrc_t add = rows_rsrc(a.addend ? static_cast<const char *>(a.addend) + at_byte : static_cast<char *>(a.out),
-                                  a.addend ? bytes : 0u);
-    if constexpr (F32) {
-#pragma unroll
-        for (int fm = 0; fm < FM; ++fm) {
-            const uint32_t r = (uint32_t)(wm * C::WM + fm * 32 + (el & 31)) * row_bytes;
-#pragma unroll
-            for (int fn = 0; fn < FN; ++fn)
-#pragma unroll
-                for (int g4 = 0; g4 < 4; ++g4) {
-                    const int c = fn * 32 + g4 * 8 + (el >> 5) * 4;
-                    const uint32_t v = c < valid ? r + (uint32_t)c * 4u : kOutOfRange;
-                    typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-                    v4u w = __builtin_amdgcn_raw_buffer_load_b128(add, (int)v, 0, 0);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        w[j] = __float_as_uint(acc[fm][fn][g4 * 4 + j] + __uint_as_float(w[j]));
-                    __builtin_amdgcn_raw_buffer_store_b128(w, dst, (int)v, 0, 0);
-                }
-        }
-    } else {
-        using FS = FragStage<C, C::LDS_BYTES>;
-        const uint32_t area = FS::area(wave, 1);
-        const int col = FS::pass_col(el);
-        const uint32_t v0 = col < valid
-                                ? (uint32_t)(wm * C::WM + FS::pass_row(0, el)) * row_bytes + 2u * (uint32_t)col
-                                : kOutOfRange;
-#pragma unroll
-        for (int fm = 0; fm < FM; ++fm) {
-            if (a.addend) {
-#pragma unroll
-                for (int p = 0; p < FS::PASSES; ++p)
-                    FS::put(area + FS::pass_off(p, el), bload8(add, v0 + (uint32_t)(fm * 32 + p * FS::RPP) * row_bytes, 0));
-            }
-#pragma unroll
-            for (int fn = 0; fn < FN; ++fn)
-#pragma unroll
-                for (int g4 = 0; g4 < 4; ++g4) {
-                    const uint32_t f = area + FS::frag_off(fn, g4, el);
-                    float y[4];
-                    const uint2 b = a.addend ? FS::get(f) : make_uint2(0, 0);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) y[j] = acc[fm][fn][g4 * 4 + j] + bf16_at(b, j);
-                    FS::put(f, make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])));
-                }
-#pragma unroll
-            for (int p = 0; p < FS::PASSES; ++p)
-                bstore8_nt(dst, v0 + (uint32_t)(fm * 32 + p * FS::RPP) * row_bytes, 0, FS::get(area + FS::pass_off(p, el)));
-        }
-    }
+    if (a.splits > 1)   // fp32 partials, joined by a second kernel
+        store_tile<C, true>(acc, t, a.N, t.part, nullptr, lds, wm, wn);
+    else
+        store_tile<C, F32>(acc, t, a.N, a.out, a.addend, lds, wm, wn);
+}
+
+__device__ __forceinline__ BlkTile matmul_tile(const BlkArgs &a, const RowTile &r, int bn) {
+    const int n0 = r.nt * bn, nb = (a.N + kBlk - 1) / kBlk, kb = (a.K + kBlk - 1) / kBlk, b0 = r.s * a.run;
+    BlkTile t;
+    t.x = a.x + (int64_t)r.m0 * a.K + b0 * kBlk;
+    t.w = a.w + ((int64_t)r.e * a.N + n0) * a.K + b0 * kBlk;
+    t.xs = a.xs + (int64_t)b0 * a.xs_ld + r.m0;
+    t.ws = a.ws + ((int64_t)r.e * nb + n0 / kBlk) * kb + b0;
+    t.rows = r.rows;
+    t.cols = min(bn, a.N - n0);
+    t.len = a.splits > 1 ? min(a.K - b0 * kBlk, a.run * kBlk) : a.K;
+    t.out = (int64_t)r.m0 * a.N + n0;
+    t.part = a.part + (int64_t)r.s * a.M * a.N;
+    return t;
+}
+__device__ __forceinline__ uint32_t lds_base() {
+    extern __shared__ __attribute__((aligned(1024))) char lds_raw[];
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds_raw;
 }
 
 template <class C, bool F32>
 __global__ __launch_bounds__(C::NT, 2) void blk_matmul(BlkArgs a) {
-    extern __shared__ __attribute__((aligned(1024))) char lds_raw[];
-    const int n_tiles = (a.N + C::BN - 1) / C::BN;
     RowTile r;
-    if (!locate(a, C::BM, n_tiles, (int)blockIdx.x, r)) return;
-    const int n0 = r.nt * C::BN, nb = (a.N + kBlk - 1) / kBlk, kb = (a.K + kBlk - 1) / kBlk;
-    BlkTile t;
-    t.x = a.x + (int64_t)r.m0 * a.K;
-    t.w = a.w + ((int64_t)r.e * a.N + n0) * a.K;
-    t.xs = a.xs + r.m0;
-    t.ws = a.ws + ((int64_t)r.e * nb + n0 / kBlk) * kb;
-    t.rows = r.rows;
-    t.cols = min(C::BN, a.N - n0);
-    t.len = a.K;
-    t.out = (int64_t)r.m0 * a.N + n0;
-    blk_tile<C, false, F32>(a, t, (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds_raw);
+    if (!locate(a, C::BM, (a.N + C::BN - 1) / C::BN, a.splits, (int)blockIdx.x, r)) return;
+    blk_tile<C, false, F32>(a, matmul_tile(a, r, C::BN), lds_base());
+}
+
+__global__ __launch_bounds__(CfgL::NT, 2) void blk_matmul_mixed(BlkArgs a) {
+    static_assert(CfgL::BN == CfgM::BN && CfgL::NT == CfgM::NT, "one grid for both");
+    RowTile r;
+    bool half;
+    if (!locate_mixed(a, (a.N + CfgL::BN - 1) / CfgL::BN, (int)blockIdx.x, r, half) || r.rows <= 0) return;
+    const BlkTile t = matmul_tile(a, r, CfgL::BN);
+    if (half) blk_tile<CfgM, false, false>(a, t, lds_base());
+    else blk_tile<CfgL, false, false>(a, t, lds_base());
 }
 
 // Weight gradients: rows of `x` are those of dy (output rows), rows of `w` those of x (columns).
 template <class C, bool F32>
 __global__ __launch_bounds__(C::NT, 2) void blk_wgrad(BlkArgs a) {
-    extern __shared__ __attribute__((aligned(1024))) char lds_raw[];
-    const int gx = (a.N + C::BN - 1) / C::BN, gy = (a.M + C::BM - 1) / C::BM;
-    const int per = (gx * gy + kXcds - 1) / kXcds * kXcds;   // workgroups of an expert
-    const int e = (int)blockIdx.x / per, b = (int)blockIdx.x % per;
-    const int id = (b % kXcds) * (per / kXcds) + b / kXcds;
-    if (id >= gx * gy) return;
-    const int gsize = kGroupM * gx, first = id / gsize * kGroupM, gm = min(kGroupM, gy - first), r = id % gsize;
-    const int m0 = (first + r % gm) * C::BM, n0 = r / gm * C::BN;
+    const int gx = (a.N + C::BN - 1) / C::BN, gy = (a.M + C::BM - 1) / C::BM, cols = gx * a.splits;
+    const int per = (cols * gy + kXcds - 1) / kXcds;
+    const int e = (int)blockIdx.x / (per * kXcds), id = xcd_tile((int)blockIdx.x % (per * kXcds), per);
+    if (id >= cols * gy) return;
+    int mt, col;
+    group_tile(id, gy, cols, mt, col);
+    const int m0 = mt * C::BM, n0 = col % gx * C::BN, s = col / gx;
     int r0 = 0, r1 = a.K;
     if (a.E > 0) {
         r0 = uniform_i(clamp_row(a.offsets[e], a.K)) & ~(kBlk - 1);
         r1 = uniform_i(clamp_row(a.offsets[e + 1], a.K));
+    }
+    if (a.splits > 1) {   // this expert's blocks in equal runs
+        const int run = ((r1 - r0 + kBlk - 1) / kBlk + a.splits - 1) / a.splits * kBlk;
+        r0 += s * run;   // past the expert's end: an empty run
+        r1 = min(r1, r0 + run);
     }
     BlkTile t;
     t.x = a.x + (int64_t)m0 * a.ld + r0;
@@ -393,7 +445,41 @@ __global__ __launch_bounds__(C::NT, 2) void blk_wgrad(BlkArgs a) {
     t.cols = min(C::BN, a.N - n0);
     t.len = max(r1 - r0, 0);
     t.out = ((int64_t)e * a.M + m0) * a.N + n0;
-    blk_tile<C, true, F32>(a, t, (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds_raw);
+    t.part = a.part + (int64_t)s * max(a.E, 1) * a.M * a.N;
+    blk_tile<C, true, F32>(a, t, lds_base());
+}
+
+// out = addend + sum of the runs' partials, in ascending order, 4 values a thread; 8 loads are in flight before the
+// first is added. Rows of no expert (products by weights) stay as they were.
+template <bool F32>
+__global__ __launch_bounds__(256) void blk_join(BlkArgs a, int64_t quads, int64_t stride, bool rows) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= quads) return;
+    if (rows && a.E > 0) {
+        const int m = (int)(i / (a.N / 4));
+        if (m < a.offsets[0] || m >= a.offsets[a.E]) return;
+    }
+    f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int r0 = 0; r0 < a.splits; r0 += 8) {
+        f32x4_t v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = *reinterpret_cast<const f32x4_t *>(a.part + min(r0 + j, a.splits - 1) * stride + i * 4);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (r0 + j < a.splits) s += v[j];
+    }
+    if constexpr (F32) {
+        if (a.addend) s += static_cast<const f32x4_t *>(a.addend)[i];
+        static_cast<f32x4_t *>(a.out)[i] = s;
+    } else {
+        if (a.addend) {
+            const uint2 b = static_cast<const uint2 *>(a.addend)[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[j] += bf16_at(b, j);
+        }
+        static_cast<uint2 *>(a.out)[i] = make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
+    }
 }
 
 template <class K>
@@ -409,28 +495,48 @@ hipError_t allow_lds(K *kernel, size_t bytes, std::atomic<uint64_t> &done) {   /
     return r;
 }
 
+// Row tiles of bm rows: at most one more for each expert that has rows.
+int64_t most_row_tiles(const BlkArgs &a, int bm) { return ceil_div(a.M, bm) + (a.E > 0 ? std::min(a.E, a.M) : 0); }
+unsigned rounded(int64_t workgroups) { return (unsigned)(ceil_div(workgroups, kXcds) * kXcds); }
+
+template <class K>
+hipError_t launch_tiles(K *kernel, const char *name, unsigned grid, int threads, size_t lds, std::atomic<uint64_t> &done,
+                        const BlkArgs &a, hipStream_t st) {
+    const hipError_t e = allow_lds(kernel, lds, done);
+    if (e != hipSuccess) return e;
+    KernelTimer tm(name, st);
+    kernel<<<grid, threads, lds, st>>>(a);
+    return hipGetLastError();
+}
+
 template <class C, bool F32>
 hipError_t launch_matmul(const BlkArgs &a, hipStream_t st) {
     static std::atomic<uint64_t> done{0};
-    const hipError_t e = allow_lds(blk_matmul<C, F32>, C::LDS_BYTES, done);
-    if (e != hipSuccess) return e;
-    // row tiles: at most one more for each expert that has rows
-    const int64_t mt = ceil_div(a.M, C::BM) + (a.E > 0 ? std::min(a.E, a.M) : 0);
-    const int64_t grid = ceil_div(mt * ceil_div(a.N, C::BN), kXcds) * kXcds;
-    KernelTimer tm("fp8_matmul", st);
-    blk_matmul<C, F32><<<(unsigned)grid, C::NT, C::LDS_BYTES, st>>>(a);
-    return hipGetLastError();
+    const unsigned grid = rounded(most_row_tiles(a, C::BM) * ceil_div(a.N, C::BN) * a.splits);
+    return launch_tiles(blk_matmul<C, F32>, "fp8_matmul", grid, C::NT, C::LDS_BYTES, done, a, st);
+}
+
+hipError_t launch_mixed(const BlkArgs &a, hipStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    // kUnits / 2 whole tiles as halves take as many workgroups again; each of the three segments is rounded up
+    const unsigned grid = rounded(most_row_tiles(a, 256) * ceil_div(a.N, CfgL::BN) + kUnits / 2) + 3 * kXcds;
+    constexpr size_t lds = CfgL::LDS_BYTES > CfgM::LDS_BYTES ? CfgL::LDS_BYTES : CfgM::LDS_BYTES;
+    return launch_tiles(blk_matmul_mixed, "fp8_matmul", grid, CfgL::NT, lds, done, a, st);
 }
 
 template <class C, bool F32>
 hipError_t launch_wgrad(const BlkArgs &a, hipStream_t st) {
     static std::atomic<uint64_t> done{0};
-    const hipError_t e = allow_lds(blk_wgrad<C, F32>, C::LDS_BYTES, done);
-    if (e != hipSuccess) return e;
-    const int64_t per = ceil_div(ceil_div(a.N, C::BN) * ceil_div(a.M, C::BM), kXcds) * kXcds;
-    const int64_t grid = per * std::max(a.E, 1);
-    KernelTimer tm("fp8_wgrad", st);
-    blk_wgrad<C, F32><<<(unsigned)grid, C::NT, C::LDS_BYTES, st>>>(a);
+    const unsigned grid =
+        rounded(ceil_div(a.N, C::BN) * ceil_div(a.M, C::BM) * a.splits) * (unsigned)std::max(a.E, 1);
+    return launch_tiles(blk_wgrad<C, F32>, "fp8_wgrad", grid, C::NT, C::LDS_BYTES, done, a, st);
+}
+
+hipError_t launch_join(const BlkArgs &a, bool f32, int64_t values, bool rows, hipStream_t st) {
+    const unsigned grid = (unsigned)ceil_div(values / 4, 256);
+    KernelTimer tm("fp8_join", st);
+    if (f32) blk_join<true><<<grid, 256, 0, st>>>(a, values / 4, values, rows);
+    else blk_join<false><<<grid, 256, 0, st>>>(a, values / 4, values, rows);
     return hipGetLastError();
 }
 
@@ -439,7 +545,6 @@ hipError_t launch_wgrad(const BlkArgs &a, hipStream_t st) {
 mok_status launch_fp8_matmul(const BlkPlan &p, void *workspace, const uint8_t *a_elems, const float *a_scales,
                              const uint8_t *b_elems, const float *b_scales, const int32_t *offsets, void *out,
                              hipStream_t st) {
-    (void)workspace;
     BlkArgs a{};
     a.xs_ld = p.M;
     a.ws_ld = (p.K + kBlk - 1) / kBlk;
@@ -449,21 +554,25 @@ mok_status launch_fp8_matmul(const BlkPlan &p, void *workspace, const uint8_t *a
     a.ws = b_scales;
     a.offsets = offsets;
     a.out = out;
+    a.part = static_cast<float *>(workspace);
     a.M = (int)p.M;
     a.N = p.N;
     a.K = p.K;
     a.E = p.E;
     a.ld = p.K;
+    a.splits = p.splits;
+    a.run = p.run;
     hipError_t e;
-    if (p.f32) e = launch_matmul<CfgM, true>(a, st);
-    else e = p.bm == CfgM::BM ? launch_matmul<CfgM, false>(a, st) : launch_matmul<CfgL, false>(a, st);
+    if (p.few) e = launch_blk_few(a, p.few, p.f32, st);
+    else if (p.bm == 256) e = launch_mixed(a, st);
+    else e = p.f32 ? launch_matmul<CfgM, true>(a, st) : launch_matmul<CfgM, false>(a, st);
+    if (e == hipSuccess && p.splits > 1) e = launch_join(a, p.f32, p.M * p.N, true, st);
     return check_hip(e, "mok_fp8_matmul");
 }
 
 mok_status launch_fp8_wgrad(const BlkPlan &p, void *workspace, const uint8_t *dy_elems, const float *dy_scales,
                             const uint8_t *x_elems, const float *x_scales, const int32_t *offsets, const void *addend,
                             void *out, hipStream_t st) {
-    (void)workspace;
     BlkArgs a{};
     a.xs_ld = p.N;
     a.ws_ld = p.K;
@@ -474,14 +583,18 @@ mok_status launch_fp8_wgrad(const BlkPlan &p, void *workspace, const uint8_t *dy
     a.offsets = offsets;
     a.addend = addend;
     a.out = out;
+    a.part = static_cast<float *>(workspace);
     a.M = p.N;
     a.N = p.K;
     a.K = (int)p.M;
     a.E = p.E;
     a.ld = (int)p.M;
+    a.splits = p.splits;
     hipError_t e;
     if (p.f32) e = launch_wgrad<CfgM, true>(a, st);
-    else e = p.bm == CfgM::BM ? launch_wgrad<CfgM, false>(a, st) : launch_wgrad<CfgL, false>(a, st);
+    else e = p.bm == 128 ? launch_wgrad<CfgM, false>(a, st) : launch_wgrad<CfgL, false>(a, st);
+    if (e == hipSuccess && p.splits > 1)
+        e = launch_join(a, p.f32, (int64_t)std::max(p.E, 1) * p.N * p.K, false, st);
     return check_hip(e, "mok_fp8_wgrad");
 }
 

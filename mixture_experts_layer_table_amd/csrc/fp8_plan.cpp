@@ -1,4 +1,17 @@
 // Plan of the products on blocks of 128: see fp8_plan.h.
+//
+// Each choice is the least estimated time in us, from the rounds of tiles over the
+// compute units, the time of a K-block, and the join of runs with its partials'
+// traffic. The constants were fitted to 32 shapes timed in a stream of calls, 1 to
+// 16,384 rows by 1,024 to 7,168 columns, one product and 4 to 16 experts. Some of
+// them, us (the choice marked *):
+//   rows x N x K          few rows       128-row tiles in 1 / 2 / 4 / 8 runs     256-row tiles
+//   1 x 4,096 x 7,168     7.6* (1 tile)  45 / 29 / 20 / 15                        45
+//   32 x 4,096 x 7,168    13.4* (2)      45 / 30 / 21 / 17                        45
+//   64 x 4,096 x 7,168    20.9 (4)       45 / 31 / 22 / 19*                       45
+//   512 x 4,096 x 7,168   147 (4)        51 / 40 / 34* / 51                       51
+//   2,048 x 7,168 x 2,048                42 / 97 / 138 / 281                      33*
+// It depends on the shape alone, so the bits of a result do too.
 #include "fp8_plan.h"
 
 #include <algorithm>
@@ -6,6 +19,15 @@
 namespace mok {
 
 namespace {
+
+constexpr int64_t kUnits = 256;              // compute units of one MI355X
+constexpr int kMostRuns = 32;
+constexpr int64_t kPartBytes = 64 << 20;     // most bytes of partials
+// Workgroups stay within one grid of fewer than 2^32 threads.
+constexpr int64_t kMostGroups = (1 << 23) - 64;
+constexpr double kTraffic = 5.0e6;           // bytes per us
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 bool widths_ok(const mok_fp8_shape *s) {
     return s && s->M >= 0 && s->N > 0 && s->K > 0 && s->N % 16 == 0 && s->K % 16 == 0 && s->N <= (1 << 20) &&
@@ -20,31 +42,101 @@ void fill(const mok_fp8_shape *s, BlkPlan *p) {
     p->K = s->K;
     p->E = s->E;
     p->f32 = s->out_dtype == MOK_STREAM_F32;
-    p->bm = 256;
+    p->bm = 128;
+    p->splits = 1;
     p->total = 256;
 }
 
-// Workgroups stay within one grid of fewer than 2^32 threads.
-constexpr int64_t kMostTiles = (1 << 23) - 64;
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+double join_us(int runs, int64_t values) { return runs == 1 ? 0.0 : 5.0 + (double)runs * values * 8 / kTraffic; }
 
 }  // namespace
 
 mok_status make_blk_matmul_plan(const mok_fp8_shape *s, BlkPlan *p) {
     if (!widths_ok(s) || s->M >= (int64_t(1) << 31)) return MOK_ERROR_INVALID_VALUE;
     fill(s, p);
-    const int64_t per = s->M / std::max(s->E, 1);   // rows of an expert in the mean
-    if (per <= 128 || p->f32) p->bm = 128;
-    if ((ceil_div(s->M, p->bm) + s->E) * ceil_div(s->N, 256) > kMostTiles) return MOK_ERROR_UNSUPPORTED;
+    const int64_t M = s->M, N = s->N, kb = ceil_div(s->K, 128), cols = ceil_div(N, 256);
+    if ((ceil_div(M, 128) + s->E) * cols > kMostGroups) return MOK_ERROR_UNSUPPORTED;
+    if (M == 0) return MOK_OK;
+    // the experts' rows are not known here: taken as equal
+    const int64_t experts = s->E > 0 ? std::min<int64_t>(s->E, M) : 1, rows = ceil_div(M, experts);
+    double least = 1e30;
+
+    // 128-row tiles, the contraction in runs
+    const int64_t tiles = experts * ceil_div(rows, 128) * cols;
+    for (int r = 1; r <= kMostRuns && r <= kb; ++r) {
+        const int64_t run = ceil_div(kb, r), groups = tiles * r;
+        if (ceil_div(kb, run) != r) continue;
+        if (r > 1 && (r * M * N * 4 > kPartBytes || (ceil_div(M, 128) + s->E) * cols * r > kMostGroups)) break;
+        const double step = (groups <= 192 ? 0.83 : 0.95) * (p->f32 ? 1.8 : 1.0);
+        const double us = 5.0 + (double)ceil_div(groups, kUnits) * (run * step + 1.0) + join_us(r, M * N);
+        if (us < least) {
+            least = us;
+            p->splits = r;
+            p->run = (int)run;
+        }
+    }
+    // 256-row tiles, with 128-row ones for an expert's last rows and the last round (bf16 results)
+    if (!p->f32) {
+        int64_t whole = experts * (rows / 256 + (rows % 256 > 128)) * cols;
+        int64_t half = experts * (rows % 256 > 0 && rows % 256 <= 128 ? 1 : 0) * cols;
+        if (whole % kUnits <= kUnits / 2) {
+            half += whole % kUnits * 2;
+            whole -= whole % kUnits;
+        }
+        half = std::max<int64_t>(half - (ceil_div(whole, kUnits) * kUnits - whole), 0);   // beside the last whole ones
+        const double us = 5.0 + (double)ceil_div(whole, kUnits) * (kb * 1.6 + 3.0) +
+                          (double)ceil_div(half, kUnits) * (kb * 0.95 + 1.0);
+        if (us < least) {
+            least = us;
+            p->bm = 256;
+            p->splits = 1;
+            p->run = 0;
+        }
+    }
+    // 16 rows of the weights a workgroup, 16 mt rows at a time
+    if (experts * N / 16 <= (1 << 22)) {
+        constexpr double rate[3] = {4.6e6, 2.8e6, 1.6e6};   // bytes of weights per us
+        for (int i = 0; i < 3; ++i) {
+            const int64_t passes = ceil_div(rows, 16 << i);
+            const double us = 3.0 + (double)passes * experts * N * s->K / rate[i];
+            if (us < least) {
+                least = us;
+                p->bm = 128;
+                p->splits = 1;
+                p->few = 1 << i;
+            }
+        }
+    }
+    if (p->splits > 1) p->total = (size_t)p->splits * M * N * 4;
     return MOK_OK;
 }
 
 mok_status make_blk_wgrad_plan(const mok_fp8_shape *s, BlkPlan *p) {
     if (!widths_ok(s) || s->M >= (int64_t(1) << 23) || s->M % 16) return MOK_ERROR_INVALID_VALUE;
     fill(s, p);
-    if (s->N <= 128 || p->f32) p->bm = 128;
-    if ((ceil_div(s->N, p->bm) * ceil_div(s->K, 256) + 8) * std::max(s->E, 1) > kMostTiles)
-        return MOK_ERROR_UNSUPPORTED;
+    const int64_t experts = std::max(s->E, 1), values = experts * s->N * s->K;
+    const int64_t kb = std::max<int64_t>(ceil_div(ceil_div(s->M, 128), experts), 1);
+    const auto groups = [&](int bm, int runs) {
+        return (ceil_div(s->N, bm) * ceil_div(s->K, 256) * runs + 8) * experts;
+    };
+    if (groups(128, 1) > kMostGroups) return MOK_ERROR_UNSUPPORTED;
+    double least = 1e30;
+    for (int bm = 128; bm <= (p->f32 ? 128 : 256); bm *= 2) {
+        const int64_t tiles = ceil_div(s->N, bm) * ceil_div(s->K, 256) * experts;
+        for (int r = 1; r <= kMostRuns && r <= kb; ++r) {
+            if (r > 1 && (r * values * 4 > kPartBytes || groups(bm, r) > kMostGroups)) break;
+            const bool filled = tiles * r > 192;
+            const double step = p->f32 ? 1.7 : bm == 128 ? (filled ? 1.1 : 0.92) : (filled ? 1.9 : 1.55);
+            const double us = 5.0 + (double)ceil_div(tiles * r, kUnits) * (ceil_div(kb, r) * step + bm / 40.0) +
+                              join_us(r, values);
+            if (us < least) {
+                least = us;
+                p->bm = bm;
+                p->splits = r;
+            }
+        }
+    }
+    if (p->splits > 1) p->total = (size_t)p->splits * values * 4;
     return MOK_OK;
 }
 

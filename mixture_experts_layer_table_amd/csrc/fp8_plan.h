@@ -12,6 +12,8 @@ struct BlkPlan {
     int N, K, E;
     bool f32;
     int bm;            // tile rows
+    int few;           // tiles of 16 rows of the few-rows kernel; 0: not taken
+    int splits, run;   // runs of the contraction, joined by a second kernel; K-blocks of one (products by weights)
     size_t total;      // workspace bytes
 };
 
