@@ -1036,6 +1036,8 @@ def _fp8_bytes(wgrad, M, N, K, E, dtype) -> int:
 
 
 def _given_workspace(workspace, need, like):
+    if workspace is None and need == 0:
+        return None
     if workspace is None:
         return like.new_empty((need,), dtype=_U8)
     _require_bytes(workspace, "workspace", need, like.device)
@@ -1073,7 +1075,7 @@ def sort_tokens(topk_ids, num_experts: int, align: int = 1, outs=None, workspace
                  row_slots=topk_ids.new_empty((rows,)))
     else:
         r = {n: outs[n] for n in ("offsets", "slots", "row_slots")}
-    _check(_lib.mok_sort_tokens(ctypes.byref(c), ws.data_ptr(), ws.numel(), topk_ids.data_ptr(),
+    _check(_lib.mok_sort_tokens(ctypes.byref(c), _addr(ws), need, topk_ids.data_ptr(),
                                 r["offsets"].data_ptr(), r["slots"].data_ptr(), r["row_slots"].data_ptr(),
                                 _raw_stream(dev.index)), "mok_sort_tokens")
     return r

@@ -444,7 +444,7 @@ mok_status mok_sort_tokens(const mok_sort_shape *shape, void *workspace, size_t 
                            void *stream) {
     SortPlan p;
     if (!shape || !sort_plan(shape->T, shape->k, shape->E, shape->align, &p)) return MOK_ERROR_INVALID_VALUE;
-    if (!dev_ok(workspace) || !dev_ok(offsets)) return MOK_ERROR_INVALID_VALUE;
+    if ((p.bytes > 0 && !dev_ok(workspace)) || !dev_ok(offsets)) return MOK_ERROR_INVALID_VALUE;
     if (p.n > 0 && (!dev_ok(topk_ids) || !dev_ok(slots) || !dev_ok(row_slots))) return MOK_ERROR_INVALID_VALUE;
     if (workspace_bytes < p.bytes) return MOK_ERROR_BUFFER_TOO_SMALL;
     const size_t n = (size_t)p.n * 4;

@@ -48,4 +48,11 @@ __device__ __forceinline__ uint32_t max16(uint32_t x) {
     return dpp_max<0x128>(x);
 }
 
+// The same of 8 neighbouring lanes.
+__device__ __forceinline__ uint32_t max8(uint32_t x) {
+    x = dpp_max<0xB1>(x);
+    x = dpp_max<0x4E>(x);
+    return dpp_max<0x141>(x);      // lane i of 8 takes lane 7 - i: equal within fours by now
+}
+
 }  // namespace mok

@@ -14,7 +14,7 @@
 #include "fp8_codec.h"
 #include "glu.h"
 #include "kernels.h"
-#include "rng.h"
+#include "stream.h"
 #include "timing.h"
 
 namespace mok {
@@ -72,8 +72,8 @@ __global__ __launch_bounds__(kQThreads) void quantize_rows(QuantArgs a) {
         s[i].values(v);   // zeros behind the row's end
         const BlkScale q = blk_scale(max16(amax8(v)));
         if (!row || c >= nc) continue;
-        reinterpret_cast<uint2 *>(a.elems)[dst_row + c] =
-            make_uint2(blk_codes4(q, v[0], v[1], v[2], v[3]), blk_codes4(q, v[4], v[5], v[6], v[7]));
+        stream8(a.elems, dst_row + c,
+                make_uint2(blk_codes4(q, v[0], v[1], v[2], v[3]), blk_codes4(q, v[4], v[5], v[6], v[7])));
         if (lane == 0) a.scales[(m * a.kblocks + kb0 + i) * a.rows + r] = q.scale;
     }
 }
@@ -113,8 +113,8 @@ __global__ __launch_bounds__(kQThreads) void quantize_tiles(QuantArgs a) {
         float v[8];
         unpack8(raw[i], v);
         if (r0 + i * 16 < a.rows && c < nc)
-            reinterpret_cast<uint2 *>(a.elems)[(m * a.rows + r0 + i * 16) * nc + c] =
-                make_uint2(blk_codes4(q, v[0], v[1], v[2], v[3]), blk_codes4(q, v[4], v[5], v[6], v[7]));
+            stream8(a.elems, (m * a.rows + r0 + i * 16) * nc + c,
+                    make_uint2(blk_codes4(q, v[0], v[1], v[2], v[3]), blk_codes4(q, v[4], v[5], v[6], v[7])));
     }
 }
 
@@ -183,7 +183,7 @@ __global__ __launch_bounds__(kQThreads) void quantize_turned(QuantArgs a) {
         if (r >= a.rows || k >= a.K) continue;
         const uint2 lo = *reinterpret_cast<const uint2 *>(codes + lr * kTurnRow + unit * 16);
         const uint2 hi = *reinterpret_cast<const uint2 *>(codes + lr * kTurnRow + unit * 16 + 8);
-        *reinterpret_cast<uint4 *>(a.elems + (m * a.rows + r) * a.K + k) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        stream16(a.elems, ((m * a.rows + r) * a.K + k) / 16, make_uint4(lo.x, lo.y, hi.x, hi.y));
     }
 }
 
@@ -218,8 +218,8 @@ __global__ __launch_bounds__(kQThreads) void glu_backward_kernel(const uint16_t 
         hg[j] = r.dg;
         hu[j] = r.du;
     }
-    store8<kBf16>(dh, g, hg);
-    store8<kBf16>(dh, u, hu);
+    stream8_elems<kBf16>(dh, g, hg);
+    stream8_elems<kBf16>(dh, u, hu);
 }
 
 }  // namespace

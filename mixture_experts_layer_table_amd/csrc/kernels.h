@@ -80,12 +80,12 @@ struct NormBackwardCall {
 int64_t norm_backward_shares(int64_t T, int H);
 mok_status launch_add_rmsnorm_backward(const NormBackwardCall &c, hipStream_t st);
 
-// The sort's path: one workgroup (`one`), or `groups` waves of `chunk` slots each.
+// The sort's path: one launch of `groups` workgroups (`few`), or `groups` waves of `chunk` slots each in three.
 struct SortPlan {
     int64_t n, rows, chunk;
     int groups;
-    bool one;
-    size_t bytes;   // workspace
+    bool few;
+    size_t bytes;   // workspace, none for few
 };
 bool sort_plan(int64_t T, int k, int E, int align, SortPlan *p);   // false: a shape outside the limits
 mok_status launch_sort_tokens(const SortPlan &p, int E, int align, const int32_t *ids, void *workspace,

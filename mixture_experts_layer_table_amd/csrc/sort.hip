@@ -8,10 +8,11 @@
 // order, rounded up to `align` and scanned over the experts. Integers only, and
 // no atomics: the table is a pure function of the ids.
 //
-// Up to kSortOne slots and kSortOneE experts, one workgroup of 16 waves does it
-// all in one launch, its counters in LDS; it is bound by its chain of barriers
-// and dependent LDS reads, not by bytes. Past that, three launches: a count per
-// wave, a scan over the waves, and the placing.
+// Up to kSortFew slots and kSortFewE experts it is one launch: workgroups of 1,024
+// slots, each of which counts all slots for itself, those ahead of its own apart.
+// Sixteen of them read the same 64 KiB from L2, which is cheaper than a second
+// launch; what bounds it is the chain of barriers and dependent accesses. Past
+// that, three launches: a count per wave, a scan over the waves, and the placing.
 #include <algorithm>
 
 #include "common.h"
@@ -21,10 +22,11 @@
 namespace mok {
 namespace {
 
-constexpr int kSortWaves = 16, kSortSteps = 16;
-constexpr int64_t kSortOne = (int64_t)kSortWaves * kSortSteps * 64;   // 16,384 slots
-constexpr int kSortOneE = 512;   // counters of 16 waves: 32 KiB of LDS
-constexpr int64_t kSortGroups = 1024;   // most waves of the three-launch form
+constexpr int kSortWaves = 16;
+constexpr int64_t kSortChunk = kSortWaves * 64;   // slots of a workgroup
+constexpr int64_t kSortFew = 32 * kSortChunk;
+constexpr int kSortFewE = 512;                    // counters of 16 waves: 32 KiB of LDS
+constexpr int64_t kSortGroups = 1024;             // most waves of the three-launch form
 
 struct SortArgs {
     const int32_t *ids;
@@ -73,30 +75,42 @@ __device__ __forceinline__ int wave_scan(int v) {   // inclusive
 
 __device__ __forceinline__ int round_up(int v, int align) { return (v + align - 1) / align * align; }
 
-__global__ __launch_bounds__(64 * kSortWaves) void sort_one(SortArgs a) {
-    __shared__ int32_t count[kSortWaves][kSortOneE + 1];
-    __shared__ int32_t first[kSortOneE + 1];
+__global__ __launch_bounds__(64 * kSortWaves) void sort_few(SortArgs a) {
+    __shared__ int32_t count[kSortWaves][kSortFewE + 1];
+    __shared__ int32_t total[kSortFewE + 1], ahead[kSortFewE + 1];   // of all slots, and of those before this workgroup's
+    __shared__ int32_t first[kSortFewE + 1];
     __shared__ int32_t wave_sum[kSortWaves];
     const int tid = (int)threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int64_t f = blockIdx.x * kSortChunk + tid;
+    const int key = sort_key(a, f);
     for (int e = lane; e <= a.E; e += 64) count[wave][e] = 0;
-    int key[kSortSteps], rank[kSortSteps];
-    const int64_t f0 = wave * a.chunk + lane;
-    const int steps = (int)(a.chunk / 64);
-#pragma unroll
-    for (int s = 0; s < kSortSteps; ++s) key[s] = s < steps ? sort_key(a, f0 + s * 64) : a.E;
-#pragma unroll
-    for (int s = 0; s < kSortSteps; ++s)
-        if (s < steps) rank[s] = take_rank(count[wave], key[s], a.bits);
+    if (tid <= a.E) total[tid] = ahead[tid] = 0;
     __syncthreads();
-    int total = 0, mine = 0;
+    const int rank = take_rank(count[wave], key, a.bits);
+    constexpr int B = 8;   // slots in flight per thread
+    for (int64_t g0 = 0; g0 < a.n; g0 += B * kSortChunk) {
+        int k[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) k[i] = sort_key(a, g0 + i * kSortChunk + tid);
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const int64_t chunk = g0 / kSortChunk + i;
+            if (chunk < (int64_t)blockIdx.x) atomicAdd(&ahead[k[i]], 1);
+            else if (chunk * kSortChunk < a.n) atomicAdd(&total[k[i]], 1);
+        }
+    }
+    __syncthreads();
+    int sum = 0, mine = 0;
     if (tid < a.E) {
+        int before = ahead[tid];
+        sum = before + total[tid];
 #pragma unroll
         for (int w = 0; w < kSortWaves; ++w) {
             const int c = count[w][tid];
-            count[w][tid] = total;
-            total += c;
+            count[w][tid] = before;
+            before += c;
         }
-        mine = round_up(total, a.align);
+        mine = round_up(sum, a.align);
     }
     int incl = wave_scan(mine);
     if (lane == 63) wave_sum[wave] = incl;
@@ -104,23 +118,21 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_one(SortArgs a) {
     for (int w = 0; w < wave; ++w) incl += wave_sum[w];
     if (tid < a.E) {
         first[tid] = incl - mine;
-        a.offsets[tid] = incl - mine;
-        for (int r = incl - mine + total; r < incl; ++r) a.row_slots[r] = -1;
+        if (blockIdx.x == 0) a.offsets[tid] = incl - mine;
+        if (tid % a.groups == (int)blockIdx.x)
+            for (int r = incl - mine + sum; r < incl; ++r) a.row_slots[r] = -1;
     }
     if (tid == a.E - 1) {
         first[a.E] = incl;
-        a.offsets[a.E] = incl;
+        if (blockIdx.x == 0) a.offsets[a.E] = incl;
     }
     __syncthreads();
-#pragma unroll
-    for (int s = 0; s < kSortSteps; ++s) {
-        const int64_t f = f0 + s * 64;
-        if (s >= steps || f >= a.n) continue;
-        const int row = key[s] < a.E ? first[key[s]] + count[wave][key[s]] + rank[s] : -1;
+    if (f < a.n) {
+        const int row = key < a.E ? first[key] + count[wave][key] + rank : -1;
         a.slots[f] = row;
         if (row >= 0) a.row_slots[row] = (int32_t)f;
     }
-    for (int64_t r = first[a.E] + tid; r < a.cap; r += 64 * kSortWaves) a.row_slots[r] = -1;
+    for (int64_t r = first[a.E] + f; r < a.cap; r += a.groups * kSortChunk) a.row_slots[r] = -1;
 }
 
 // Slots per expert of this wave's chunk.
@@ -191,11 +203,11 @@ bool sort_plan(int64_t T, int k, int E, int align, SortPlan *p) {
     if (n >= (int64_t(1) << 31) || rows >= (int64_t(1) << 31)) return false;
     p->n = n;
     p->rows = rows;
-    p->one = n <= kSortOne && E <= kSortOneE;
-    const int64_t waves = p->one ? kSortWaves : std::max<int64_t>(1, std::min(kSortGroups, (n + 1023) / 1024));
-    p->chunk = std::max<int64_t>(64, (n + waves * 64 - 1) / (waves * 64) * 64);
-    p->groups = p->one ? 1 : (int)std::max<int64_t>(1, (n + p->chunk - 1) / p->chunk);
-    p->bytes = p->one ? 256 : std::max<size_t>(256, ((size_t)p->groups + 1) * E * 4);
+    p->few = n <= kSortFew && E <= kSortFewE;
+    const int64_t waves = std::max<int64_t>(1, std::min(kSortGroups, (n + 1023) / 1024));
+    p->chunk = p->few ? kSortChunk : std::max<int64_t>(64, (n + waves * 64 - 1) / (waves * 64) * 64);
+    p->groups = (int)std::max<int64_t>(1, (n + p->chunk - 1) / p->chunk);
+    p->bytes = p->few ? 0 : ((size_t)p->groups + 1) * E * 4;
     return true;
 }
 
@@ -216,8 +228,8 @@ mok_status launch_sort_tokens(const SortPlan &p, int E, int align, const int32_t
     a.groups = p.groups;
     while ((1 << a.bits) <= E) ++a.bits;   // keys 0 .. E
     KernelTimer tm("sort_tokens", st);
-    if (p.one) {
-        sort_one<<<1, 64 * kSortWaves, 0, st>>>(a);
+    if (p.few) {
+        sort_few<<<(unsigned)p.groups, 64 * kSortWaves, 0, st>>>(a);
     } else {
         const size_t lds = ((size_t)E + 1) * 4;
         sort_count<<<(unsigned)p.groups, 64, lds, st>>>(a);
