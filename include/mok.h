@@ -659,7 +659,8 @@ typedef struct mok_fp8_shape {
     int32_t N, K, E, out_dtype;
 } mok_fp8_shape;
 
-/* Host-only: workspace bytes of mok_fp8_matmul and mok_fp8_wgrad. */
+/* Host-only: workspace bytes of mok_fp8_matmul and mok_fp8_wgrad (0 where the
+   contraction is not cut into runs: the workspace may then be NULL). */
 mok_status mok_fp8_matmul_size(const mok_fp8_shape *shape, size_t *workspace_bytes);
 mok_status mok_fp8_wgrad_size(const mok_fp8_shape *shape, size_t *workspace_bytes);
 

@@ -1084,20 +1084,25 @@ def sort_tokens(topk_ids, num_experts: int, align: int = 1, outs=None, workspace
 def _sort_of(sort, device):
     """(T, k, rows, E) of a sort_tokens() dict, its tensors checked."""
     slots, row_slots, offsets = sort["slots"], sort["row_slots"], sort["offsets"]
-    if slots.dim() != 2 or row_slots.dim() != 1 or offsets.dim() != 1 or offsets.shape[0] < 2:
+    shape = slots.shape
+    if len(shape) != 2 or row_slots.dim() != 1 or offsets.dim() != 1 or offsets.numel() < 2:
         raise ValueError("sort: expected slots [T, k], row_slots [rows] and offsets [E + 1]")
-    _need(slots, "slots", _I32, slots.shape, device)
-    _need(row_slots, "row_slots", _I32, row_slots.shape, device)
-    _need(offsets, "offsets", _I32, offsets.shape, device)
-    return slots.shape[0], slots.shape[1], row_slots.shape[0], offsets.shape[0] - 1
+    if not (slots.dtype is _I32 and row_slots.dtype is _I32 and offsets.dtype is _I32 and slots.is_contiguous()
+            and row_slots.is_contiguous() and offsets.is_contiguous() and slots.device == device
+            and row_slots.device == device and offsets.device == device):
+        for t, name in ((slots, "slots"), (row_slots, "row_slots"), (offsets, "offsets")):
+            _require(t, name, _I32, t.shape, device)
+    return shape[0], shape[1], row_slots.numel(), offsets.numel() - 1
 
 
-def _rows_of(t, name, n, dtype=None, device=None):
+def _rows_of(t, name, n):
     """H of a tensor of n rows, checked."""
-    if t.dim() != 2 or t.shape[0] != n:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{n}, H]")
-    _need(t, name, t.dtype if dtype is None else dtype, t.shape, t.device if device is None else device)
-    return t.shape[1]
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != n:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected [{n}, H]")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return shape[1]
 
 
 def permute(x, sort, rows: bool = True, fp8: bool = False, outs=None):
@@ -1219,15 +1224,16 @@ def fp8_quantize(src, src_is_k_by_rows: bool = False, tile: bool = False, glu: b
     if src.dim() != 3:
         raise ValueError(f"src: expected [B, rows, K] or [B, K, rows], got shape {tuple(src.shape)}")
     sd = _stream_dtype(src.dtype, "src")
-    _need(src, "src", src.dtype, src.shape, dev)
-    B, last = src.shape[0], src.shape[2]
+    if not src.is_contiguous():
+        raise ValueError("src: must be contiguous")
+    B, middle, last = src.shape
     if glu:
         if tile or sd != MOK_STREAM_BF16:
             raise ValueError("glu takes bf16 rows and no tile")
         if last % 2:
             raise ValueError(f"src: last dimension {last}, expected two halves")
         last //= 2
-    rows, K = (last, src.shape[1]) if src_is_k_by_rows else (src.shape[1], last)
+    rows, K = (last, middle) if src_is_k_by_rows else (middle, last)
     if K % 16 or (src_is_k_by_rows and rows % 8):
         raise ValueError(f"src: K = {K}, rows = {rows}: K must be a multiple of 16"
                          + (" and rows of 8" if src_is_k_by_rows else ""))
@@ -1280,12 +1286,15 @@ def _row_codes(t, name, device=None):
     el, sc = _pair(t, name)
     if el.dim() == 3 and el.shape[0] == 1 and sc.dim() == 3:
         el, sc = el[0], sc[0]
-    if el.dim() != 2:
-        raise ValueError(f"{name} elems: shape {tuple(el.shape)}, expected [rows, K]")
+    shape = el.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} elems: shape {tuple(shape)}, expected [rows, K]")
+    rows, K = shape
     dev = el.device if device is None else device
-    _need(el, name + " elems", _U8, el.shape, dev)
-    _need(sc, name + " scales", _F32, ((el.shape[1] + 127) // 128, el.shape[0]), dev)
-    return el, sc, el.shape[0], el.shape[1]
+    if not (el.dtype is _U8 and el.is_contiguous() and (device is None or el.device == dev)):
+        _require(el, name + " elems", _U8, shape, dev)
+    _need(sc, name + " scales", _F32, ((K + 127) // 128, rows), dev)
+    return el, sc, rows, K
 
 
 def _experts(offsets, device):
@@ -1330,7 +1339,7 @@ def fp8_matmul(a, b, offsets=None, out_dtype=torch.bfloat16, out=None, workspace
     ws = _given_workspace(workspace, need, el)
     if out is None:
         out = el.new_empty((M, N), dtype=out_dtype)
-    _check(_lib.mok_fp8_matmul(ctypes.byref(_fp8_shape(M, N, K, E, sd)), ws.data_ptr(), ws.numel(), el.data_ptr(),
+    _check(_lib.mok_fp8_matmul(ctypes.byref(_fp8_shape(M, N, K, E, sd)), _addr(ws), need, el.data_ptr(),
                                sc.data_ptr(), bel.data_ptr(), bsc.data_ptr(), _addr(offsets), out.data_ptr(),
                                _raw_stream(dev.index)), "mok_fp8_matmul")
     return out
@@ -1366,7 +1375,7 @@ def fp8_wgrad(dy, x, offsets=None, out_dtype=torch.bfloat16, addend=None, out=No
     ws = _given_workspace(workspace, need, el)
     if out is None:
         out = el.new_empty(shape, dtype=out_dtype)
-    _check(_lib.mok_fp8_wgrad(ctypes.byref(_fp8_shape(R, N, K, E, sd)), ws.data_ptr(), ws.numel(), el.data_ptr(),
+    _check(_lib.mok_fp8_wgrad(ctypes.byref(_fp8_shape(R, N, K, E, sd)), _addr(ws), need, el.data_ptr(),
                               sc.data_ptr(), xel.data_ptr(), xsc.data_ptr(), _addr(offsets), _addr(addend),
                               out.data_ptr(), _raw_stream(dev.index)), "mok_fp8_wgrad")
     return out

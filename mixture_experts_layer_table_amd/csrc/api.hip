@@ -599,7 +599,7 @@ mok_status mok_fp8_matmul(const mok_fp8_shape *shape, void *workspace, size_t wo
     BlkPlan p;
     const mok_status s = make_blk_matmul_plan(shape, &p);
     if (s != MOK_OK) return s;
-    if (!dev_ok(workspace) || !dev_ok(b_elems) || !dev_ok(b_scales) || (p.E > 0 ? !dev_ok(offsets) : offsets != nullptr))
+    if ((p.total > 0 && !dev_ok(workspace)) || !dev_ok(b_elems) || !dev_ok(b_scales) || (p.E > 0 ? !dev_ok(offsets) : offsets != nullptr))
         return MOK_ERROR_INVALID_VALUE;
     if (p.M > 0 && (!dev_ok(a_elems) || !dev_ok(a_scales) || !dev_ok(out))) return MOK_ERROR_INVALID_VALUE;
     if (workspace_bytes < p.total) return MOK_ERROR_BUFFER_TOO_SMALL;
@@ -620,7 +620,7 @@ mok_status mok_fp8_wgrad(const mok_fp8_shape *shape, void *workspace, size_t wor
     BlkPlan p;
     const mok_status s = make_blk_wgrad_plan(shape, &p);
     if (s != MOK_OK) return s;
-    if (!dev_ok(workspace) || !dev_ok(out) || !dev_ok_or_null(addend) ||
+    if ((p.total > 0 && !dev_ok(workspace)) || !dev_ok(out) || !dev_ok_or_null(addend) ||
         (p.E > 0 ? !dev_ok(offsets) : offsets != nullptr))
         return MOK_ERROR_INVALID_VALUE;
     if (p.M > 0 && (!dev_ok(dy_elems) || !dev_ok(dy_scales) || !dev_ok(x_elems) || !dev_ok(x_scales)))

@@ -44,7 +44,6 @@ void fill(const mok_fp8_shape *s, BlkPlan *p) {
     p->f32 = s->out_dtype == MOK_STREAM_F32;
     p->bm = 128;
     p->splits = 1;
-    p->total = 256;
 }
 
 double join_us(int runs, int64_t values) { return runs == 1 ? 0.0 : 5.0 + (double)runs * values * 8 / kTraffic; }

@@ -14,7 +14,7 @@ struct BlkPlan {
     int bm;            // tile rows
     int few;           // tiles of 16 rows of the few-rows kernel; 0: not taken
     int splits, run;   // runs of the contraction, joined by a second kernel; K-blocks of one (products by weights)
-    size_t total;      // workspace bytes
+    size_t total;      // workspace bytes (0: none)
 };
 
 mok_status make_blk_matmul_plan(const mok_fp8_shape *s, BlkPlan *p);

@@ -79,7 +79,7 @@ def test_every_plan_can_run(plan):
                         assert (M // 128 + E) * (N // 256) >= 1 << 22
                         continue
                     kb = -(-K // 128)
-                    assert p.bm in (128, 256) and p.few in (0, 1, 2, 4) and p.total >= 256
+                    assert p.bm in (128, 256) and p.few in (0, 1, 2, 4) and (p.total > 0) == (p.splits > 1)
                     assert not (f32 and p.bm == 256)
                     if p.splits > 1:
                         assert p.bm == 128 and p.few == 0 and -(-kb // p.run) == p.splits

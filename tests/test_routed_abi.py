@@ -189,9 +189,9 @@ def _matmul(shape=None, **over):
     return mok.mok_fp8_matmul(_fp8(**(shape or {})), *k.values(), None)
 
 
-@pytest.mark.parametrize("over", [dict(ws=None), dict(a=None), dict(asc=None), dict(b=None), dict(bsc=None),
+@pytest.mark.parametrize("over", [dict(a=None), dict(asc=None), dict(b=None), dict(bsc=None),
                                   dict(out=None), dict(offsets=_a(6)), dict(a=_a(1) + 8), dict(out=_a(1)),
-                                  dict(out=_a(3) + 16), dict(out=_a(0)), dict(ws=_a(2)), dict(out=_a(4))])
+                                  dict(out=_a(3) + 16), dict(out=_a(2)), dict(out=_a(4))])
 def test_matmul_refuses_buffers(over):
     assert _matmul(**over) == BAD
 
@@ -199,7 +199,10 @@ def test_matmul_refuses_buffers(over):
 def test_matmul_refuses_missing_offsets_and_small_workspaces():
     assert _matmul(dict(E=2)) == BAD
     assert _matmul(dict(E=2), offsets=_a(5)) == BAD          # the output's buffer
-    assert _matmul(n=0) == SMALL
+    runs = dict(M=128, N=2064, K=7168)                       # a contraction in runs: with a workspace
+    assert _matmul(runs, n=0) == SMALL
+    for ws in (None, _a(0) + 8, _a(1), _a(3), _a(5)):
+        assert _matmul(runs, ws=ws) == BAD
     assert _matmul(dict(M=0), a=None, asc=None, out=None) == mok.MOK_OK
 
 
@@ -209,15 +212,19 @@ def _wgrad(shape=None, **over):
     return mok.mok_fp8_wgrad(_fp8(**(shape or {})), *k.values(), None)
 
 
-@pytest.mark.parametrize("over", [dict(ws=None), dict(dy=None), dict(dysc=None), dict(x=None), dict(xsc=None),
+@pytest.mark.parametrize("over", [dict(dy=None), dict(dysc=None), dict(x=None), dict(xsc=None),
                                   dict(out=None), dict(offsets=_a(7)), dict(addend=_a(6) + 2), dict(out=_a(1)),
-                                  dict(out=_a(6) + 16), dict(out=_a(3)), dict(ws=_a(6))])
+                                  dict(out=_a(6) + 16), dict(out=_a(3))])
 def test_wgrad_refuses_buffers(over):
     assert _wgrad(**over) == BAD
 
 
 def test_wgrad_refuses_missing_offsets_and_small_workspaces():
-    assert _wgrad(dict(E=3)) == BAD and _wgrad(n=0) == SMALL
+    assert _wgrad(dict(E=3)) == BAD
+    runs = dict(M=8192, N=512, K=512)                        # a contraction in runs: with a workspace
+    assert _wgrad(runs, n=0) == SMALL
+    for ws in (None, _a(0) + 8, _a(1), _a(4), _a(5), _a(6)):
+        assert _wgrad(runs, ws=ws) == BAD
 
 
 # ------------------------------------------------------------------------- the binding
