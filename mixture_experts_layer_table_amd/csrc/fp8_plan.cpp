@@ -24,7 +24,7 @@ constexpr int64_t kUnits = 256;              // compute units of one MI355X
 constexpr int kMostRuns = 32;
 constexpr int64_t kPartBytes = 64 << 20;     // most bytes of partials
 // Workgroups stay within one grid of fewer than 2^32 threads.
-constexpr int64_t kMostGroups = (1 << 23) - 64;
+constexpr int64_t kMostGroups = (1 << 23) - 512;
 constexpr double kTraffic = 5.0e6;           // bytes per us
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

@@ -21,7 +21,7 @@ namespace mok {
 namespace {
 
 constexpr int kQThreads = 256;
-constexpr int kRun = 4;                     // blocks of a row in flight per thread
+constexpr int kRun = 2;                     // blocks of a row per thread (16,384 x 7,168: 1, 2, 4 blocks 69, 62, 65 us)
 constexpr int64_t kMostGroups = 1 << 23;    // workgroups of a launch: a grid takes fewer than 2^32 threads
 
 struct QuantArgs {

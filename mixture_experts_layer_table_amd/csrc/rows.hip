@@ -22,7 +22,9 @@ namespace mok {
 namespace {
 
 constexpr int kRowThreads = 256;            // a chunk of 8 elements each
-constexpr int kPadRows = 32;                // rows that a workgroup looks over for padding, 8 a wave
+// Rows that a wave and a workgroup look over for padding. Two a wave: an expert's padding is one run of rows, and a
+// wave that fills eight of them ends last (1,001 x 4,096 in fp32, two rows a token, 128-row runs: 22 against 16 us).
+constexpr int kPadWave = 2, kPadRows = kPadWave * kRowThreads / 64;
 constexpr int kBatch = 8;                   // rows in flight per thread
 constexpr int64_t kMostGroups = 1 << 23;    // workgroups of a launch: a grid takes fewer than 2^32 threads
 
@@ -40,13 +42,26 @@ struct RowsArgs {
 
 __device__ __forceinline__ bool row_ok(const RowsCall &c, int64_t row) { return (uint64_t)row < (uint64_t)c.rows; }
 
-// Zeros into the padding rows among rows [r0, r0 + 8) of this wave.
+// The rows (or -1) of slots [j0, j0 + N) of token t, read ahead of any store: a load behind one would be made again.
+template <int N>
+struct SlotRows {
+    int r[N];
+    __device__ __forceinline__ SlotRows(const RowsCall &c, int64_t t, int j0) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            r[j] = j0 + j < c.k ? c.slots[t * c.k + j0 + j] : -1;
+            if (!row_ok(c, r[j])) r[j] = -1;
+        }
+    }
+};
+
+// Zeros into the padding rows among this wave's.
 template <Elem E, bool ROWS, bool FP8>
 __device__ __forceinline__ void pad_rows(const RowsArgs &a, int64_t group) {
     const RowsCall &c = a.c;
     const int lane = (int)(threadIdx.x & 63), nc = c.H / 8;
-    const int64_t r0 = group * kPadRows + (threadIdx.x >> 6) * 8, end = min((int64_t)c.offsets[c.E], c.rows);
-    for (int i = 0; i < 8; ++i) {
+    const int64_t r0 = group * kPadRows + (threadIdx.x >> 6) * kPadWave, end = min((int64_t)c.offsets[c.E], c.rows);
+    for (int i = 0; i < kPadWave; ++i) {
         const int64_t r = r0 + i;
         if (r >= end) return;
         if (c.row_slots[r] >= 0) continue;
@@ -73,16 +88,17 @@ __global__ __launch_bounds__(kRowThreads) void permute_kernel(RowsArgs a) {
     const int nc = c.H / 8, h = (int)(b % a.strips) * kRowThreads + (int)threadIdx.x;
     if (h >= nc) return;
     const Raw8<E> v = load8<E>(a.x, t * nc + h);
-    const int32_t *slots = c.slots + t * c.k;
-    for (int j = 0; j < c.k; ++j) {
-        const int64_t r = slots[j];
-        if (row_ok(c, r)) stream8_raw<E>(a.rows, r * nc + h, v);
+    for (int j0 = 0; j0 < c.k; j0 += kBatch) {
+        const SlotRows<kBatch> s(c, t, j0);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            if (s.r[j] >= 0) stream8_raw<E>(a.rows, (int64_t)s.r[j] * nc + h, v);
     }
 }
 
 // The row quantized (and as it is, with ROWS): 16 elements a thread, 8 neighbouring
 // lanes a block. H is a multiple of 16. 16-byte stores of codes instead of 8-byte
-// ones: 2,048 x 7,168 to 8 rows each, with non-temporal ones, 44 -> 34 us.
+// ones: 2,048 x 7,168 to 8 rows each, with non-temporal ones, 44 -> 31 us.
 template <Elem E, bool ROWS>
 __global__ __launch_bounds__(kRowThreads) void permute_quantized(RowsArgs a) {
     const RowsCall &c = a.c;
@@ -106,16 +122,19 @@ __global__ __launch_bounds__(kRowThreads) void permute_quantized(RowsArgs a) {
     const uint4 q = make_uint4(blk_codes4(s, v[0], v[1], v[2], v[3]), blk_codes4(s, v[4], v[5], v[6], v[7]),
                                blk_codes4(s, w[0], w[1], w[2], w[3]), blk_codes4(s, w[4], w[5], w[6], w[7]));
     if (!live) return;
-    const int32_t *slots = c.slots + t * c.k;
-    for (int j = 0; j < c.k; ++j) {
-        const int64_t r = slots[j];
-        if (!row_ok(c, r)) continue;
-        if constexpr (ROWS) {
-            stream8_raw<E>(a.rows, (r * nu + u) * 2, lo);
-            stream8_raw<E>(a.rows, (r * nu + u) * 2 + 1, hi);
+    for (int j0 = 0; j0 < c.k; j0 += kBatch) {
+        const SlotRows<kBatch> to(c, t, j0);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int64_t r = to.r[j];
+            if (r < 0) continue;
+            if constexpr (ROWS) {
+                stream8_raw<E>(a.rows, (r * nu + u) * 2, lo);
+                stream8_raw<E>(a.rows, (r * nu + u) * 2 + 1, hi);
+            }
+            stream16(a.elems, r * nu + u, q);
+            if (u % 8 == 0) a.scales[u / 8 * c.rows + r] = s.scale;
         }
-        stream16(a.elems, r * nu + u, q);
-        if (u % 8 == 0) a.scales[u / 8 * c.rows + r] = s.scale;
     }
 }
 
@@ -128,16 +147,14 @@ __global__ __launch_bounds__(kRowThreads) void unpermute_kernel(RowsArgs a) {
     float s[8] = {}, add[8] = {};
     if (a.addend) unpack8(load8<E>(a.addend, t * nc + h), add);
     for (int j0 = 0; j0 < c.k; j0 += kBatch) {
+        const SlotRows<kBatch> from(c, t, j0);
         Raw8<E> raw[kBatch] = {};
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const int64_t r = j0 + j < c.k ? c.slots[t * c.k + j0 + j] : -1;
-            if (row_ok(c, r)) raw[j] = load8<E>(a.y, r * nc + h);
-        }
+        for (int j = 0; j < kBatch; ++j)
+            if (from.r[j] >= 0) raw[j] = load8<E>(a.y, (int64_t)from.r[j] * nc + h);
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-            const int64_t r = j0 + j < c.k ? c.slots[t * c.k + j0 + j] : -1;
-            if (!row_ok(c, r)) continue;   // nothing, whatever its weight
+            if (from.r[j] < 0) continue;   // nothing, whatever its weight
             float v[8], w = 1.0f;
             if constexpr (W) w = a.w[t * c.k + j0 + j];
             unpack8(raw[j], v);
@@ -167,7 +184,10 @@ __global__ __launch_bounds__(kRowThreads) void unpermute_backward_kernel(RowsArg
     const int64_t t = b;
     const int nc = c.H / 8, tid = (int)threadIdx.x, wave = tid >> 6;
     for (int j0 = 0; j0 < c.k; j0 += NB) {
-        float dot[NB] = {};
+        const SlotRows<NB> to(c, t, j0);
+        float dot[NB] = {}, w[NB];
+#pragma unroll
+        for (int j = 0; j < NB; ++j) w[j] = to.r[j] >= 0 ? a.w[t * c.k + j0 + j] : 0.0f;
         for (int h0 = tid; h0 < nc; h0 += CH * kRowThreads) {
             Raw8<E> dr[CH] = {}, yr[CH][NB] = {};
 #pragma unroll
@@ -175,10 +195,8 @@ __global__ __launch_bounds__(kRowThreads) void unpermute_backward_kernel(RowsArg
                 const int h = h0 + i * kRowThreads;
                 if (h < nc) dr[i] = load8<E>(a.x, t * nc + h);
 #pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    const int64_t r = j0 + j < c.k ? c.slots[t * c.k + j0 + j] : -1;
-                    if (h < nc && row_ok(c, r)) yr[i][j] = load8<E>(a.y, r * nc + h);
-                }
+                for (int j = 0; j < NB; ++j)
+                    if (h < nc && to.r[j] >= 0) yr[i][j] = load8<E>(a.y, (int64_t)to.r[j] * nc + h);
             }
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
@@ -187,17 +205,16 @@ __global__ __launch_bounds__(kRowThreads) void unpermute_backward_kernel(RowsArg
                 unpack8(dr[i], d);
 #pragma unroll
                 for (int j = 0; j < NB; ++j) {
-                    const int64_t r = j0 + j < c.k ? c.slots[t * c.k + j0 + j] : -1;
-                    if (h >= nc || !row_ok(c, r)) continue;
-                    const float w = a.w[t * c.k + j0 + j];
+                    if (h >= nc || to.r[j] < 0) continue;
                     float v[8], g[8];
                     unpack8(yr[i][j], v);
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
                         dot[j] = __builtin_fmaf(d[q], v[q], dot[j]);
-                        g[q] = w * d[q];
+                        g[q] = w[j] * d[q];
                     }
-                    stream8_elems<E>(a.rows, r * nc + h, g);   // y's own chunk may lie here: read above, by this thread alone
+                    // y's own chunk may lie here: read above, by this thread alone
+                    stream8_elems<E>(a.rows, (int64_t)to.r[j] * nc + h, g);
                 }
             }
         }
@@ -211,7 +228,7 @@ __global__ __launch_bounds__(kRowThreads) void unpermute_backward_kernel(RowsArg
             float s = 0.0f;
 #pragma unroll
             for (int w = 0; w < kRowThreads / 64; ++w) s += red[w][tid];
-            a.dw[t * c.k + j0 + tid] = row_ok(c, c.slots[t * c.k + j0 + tid]) ? s : 0.0f;
+            a.dw[t * c.k + j0 + tid] = s;   // 0 for a slot without a row
         }
         __syncthreads();
     }
