@@ -2,12 +2,18 @@
 // are read once, straight into registers, and bound the time.
 //
 // A workgroup takes 16 rows of W (of one expert) over the whole contraction, its 8
-// waves K-blocks in turn, so that together they read whole runs of the 16 rows.
-// A wave asks for kAhead K-blocks at once: 16 rows x 128 bytes each, two 16-byte
-// loads a lane, and the same of up to 16 MT rows of X (rows past the last read as
-// zeros). v_mfma_f32_16x16x128_f8f6f4 (rows n, columns m) makes a block's product
-// from zero; the scales join it to the accumulator as in fp8_gemm.h, and the
-// waves' sums are added through LDS in order.
+// waves K-blocks in turn, so that together they read whole runs of the 16 rows. A
+// wave holds one K-block: 16 rows x 128 bytes, two 16-byte loads a lane, and the
+// same of up to 16 MT rows of X (rows past the last read as zeros).
+// v_mfma_f32_16x16x128_f8f6f4 (rows n, columns m) makes a block's product from
+// zero; the scales join it to the accumulator as in fp8_gemm.h, and the waves' sums
+// are added through LDS in order.
+//
+// One block a wave keeps the registers few (MT = 1: 40), so that four workgroups
+// share a compute unit and their loads overlap; seven blocks in flight a wave took
+// the same time for one round of workgroups (1 row x 4,096 x 7,168: 7.9 against 7.8
+// us, 3.8 TB/s with its launch) and 124 against 46 us for 28 rounds of short rows (16
+// experts of one row each, 7,168 x 2,048; 5.1 TB/s).
 #include "fp8_plan.h"
 #include "fp8_tiles.h"
 
@@ -37,8 +43,8 @@ __device__ __forceinline__ i32x8v_t load_block(brsrc_t r, uint32_t lo, uint32_t 
     return i32x8v_t{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
 
-// MT: tiles of 16 rows of X at a time. AHEAD: K-blocks a wave asks for at once.
-template <int MT, int AHEAD, bool F32>
+// MT: tiles of 16 rows of X at a time.
+template <int MT, bool F32>
 __global__ __launch_bounds__(64 * kFewWaves) void blk_few(BlkArgs a) {
     __shared__ __attribute__((aligned(16))) float red[kFewWaves][MT * 16][16];
     const int strips = a.N / 16, n0 = (int)blockIdx.x % strips * 16;
@@ -57,37 +63,29 @@ __global__ __launch_bounds__(64 * kFewWaves) void blk_few(BlkArgs a) {
         f32x4_t acc[MT];
 #pragma unroll
         for (int t = 0; t < MT; ++t) acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int k0 = wave; k0 < nk; k0 += kFewWaves * AHEAD) {
-            i32x8v_t w[AHEAD], x[AHEAD][MT];
-            float sw[AHEAD], sx[AHEAD][MT];
+        for (int kb = wave; kb < nk; kb += kFewWaves) {
+            const int at = kb * kBlk;
+            // what lies behind a row's end is another row's: zeros instead
+            const bool l = at + q * 16 < a.K, h = at + 64 + q * 16 < a.K;
+            const i32x8v_t w = load_block(wr, l ? own : kOutOfRange, h ? own + 64u : kOutOfRange, (uint32_t)at);
+            i32x8v_t x[MT];
+            float sx[MT];
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-                const int kb = k0 + i * kFewWaves;
-                const bool in = kb < nk;
-                const int at = in ? kb * kBlk : 0;
-                // what lies behind a row's end is another row's: zeros instead
-                const bool l = in && at + q * 16 < a.K, h = in && at + 64 + q * 16 < a.K;
-                w[i] = load_block(wr, l ? own : kOutOfRange, h ? own + 64u : kOutOfRange, (uint32_t)at);
-#pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    const uint32_t o = own + (uint32_t)t * 16u * (uint32_t)a.K;
-                    x[i][t] = load_block(xr, l ? o : kOutOfRange, h ? o + 64u : kOutOfRange, (uint32_t)at);
-                }
-                sw[i] = ws[in ? kb : 0];
-                const float *s = a.xs + (int64_t)(in ? kb : 0) * a.xs_ld + m0;
-#pragma unroll
-                for (int t = 0; t < MT; ++t) sx[i][t] = s[min(t * 16 + row, rows - 1)];
+            for (int t = 0; t < MT; ++t) {
+                const uint32_t o = own + (uint32_t)t * 16u * (uint32_t)a.K;
+                x[t] = load_block(xr, l ? o : kOutOfRange, h ? o + 64u : kOutOfRange, (uint32_t)at);
             }
+            const float sw = ws[kb], *s = a.xs + (int64_t)kb * a.xs_ld + m0;
+#pragma unroll
+            for (int t = 0; t < MT; ++t) sx[t] = s[min(t * 16 + row, rows - 1)];
             __builtin_amdgcn_sched_barrier(0);   // all of them in flight before the first product
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i)
+            for (int t = 0; t < MT; ++t) {
+                const f32x4_t p = few_product<F32>(w, x[t]);
+                const float both = sw * sx[t];
 #pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    const f32x4_t p = few_product<F32>(w[i], x[i][t]);
-                    const float s = sw[i] * sx[i][t];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[t][j] = __builtin_fmaf(p[j], s, acc[t][j]);
-                }
+                for (int j = 0; j < 4; ++j) acc[t][j] = __builtin_fmaf(p[j], both, acc[t][j]);
+            }
         }
 #pragma unroll
         for (int t = 0; t < MT; ++t) *reinterpret_cast<f32x4_t *>(&red[wave][t * 16 + row][q * 4]) = acc[t];
@@ -110,21 +108,21 @@ __global__ __launch_bounds__(64 * kFewWaves) void blk_few(BlkArgs a) {
     }
 }
 
-template <int MT, int AHEAD>
+template <int MT>
 hipError_t launch_few(const BlkArgs &a, bool f32, hipStream_t st) {
     const unsigned grid = (unsigned)(a.N / 16) * (unsigned)(a.E > 0 ? std::min(a.E, a.M) : 1);
     KernelTimer tm("fp8_matmul_few", st);
     if (f32)
-        blk_few<MT, AHEAD, true><<<grid, 64 * kFewWaves, 0, st>>>(a);
+        blk_few<MT, true><<<grid, 64 * kFewWaves, 0, st>>>(a);
     else
-        blk_few<MT, AHEAD, false><<<grid, 64 * kFewWaves, 0, st>>>(a);
+        blk_few<MT, false><<<grid, 64 * kFewWaves, 0, st>>>(a);
     return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_blk_few(const BlkArgs &a, int mt, bool f32, hipStream_t st) {
-    return mt == 1 ? launch_few<1, 7>(a, f32, st) : mt == 2 ? launch_few<2, 4>(a, f32, st) : launch_few<4, 2>(a, f32, st);
+    return mt == 1 ? launch_few<1>(a, f32, st) : mt == 2 ? launch_few<2>(a, f32, st) : launch_few<4>(a, f32, st);
 }
 
 }  // namespace mok

@@ -1,16 +1,18 @@
 // Plan of the products on blocks of 128: see fp8_plan.h.
 //
 // Each choice is the least estimated time in us, from the rounds of tiles over the
-// compute units, the time of a K-block, and the join of runs with its partials'
-// traffic. The constants were fitted to 32 shapes timed in a stream of calls, 1 to
-// 16,384 rows by 1,024 to 7,168 columns, one product and 4 to 16 experts. Some of
-// them, us (the choice marked *):
-//   rows x N x K          few rows       128-row tiles in 1 / 2 / 4 / 8 runs     256-row tiles
-//   1 x 4,096 x 7,168     7.6* (1 tile)  45 / 29 / 20 / 15                        45
-//   32 x 4,096 x 7,168    13.4* (2)      45 / 30 / 21 / 17                        45
-//   64 x 4,096 x 7,168    20.9 (4)       45 / 31 / 22 / 19*                       45
-//   512 x 4,096 x 7,168   147 (4)        51 / 40 / 34* / 51                       51
-//   2,048 x 7,168 x 2,048                42 / 97 / 138 / 281                      33*
+// compute units, the time of a K-block, the weights' bytes, and the join of runs with
+// its partials' traffic. The constants were fitted to some 40 shapes timed in a graph
+// of calls, 1 to 16,384 rows by 1,024 to 14,336 columns, one product and 4 to 16
+// experts. Some of them, us (the choice marked *):
+//   rows x N x K              few rows at 16 / 32 / 64   128-row tiles in 1 / 4 / 8 runs   256-row tiles
+//   1 x 4,096 x 7,168         7.7* / 8.7 / 11.2          44 / 19 / 14                      44
+//   32 x 4,096 x 7,168        16.3 / 12.7* / 16.3        44 / 20 / 15.5                    45
+//   64 x 7,168 x 2,048        18.7 / 15.3 / 13.4*        16.9 / 15.6 / 18.9                17.1
+//   64 x 4,096 x 7,168        33 / 27 / 26               44 / 20.7 / 17.3*                 45
+//   512 x 4,096 x 7,168       228 / 170 / 162            50 / 32* / 48                     51
+//   2,048 x 7,168 x 2,048     495 / 387 / 311            41 / 122 / 242                    33*
+//   16 of 16 experts, 7,168 x 2,048   45.5* / 54 / 82    47.7 / 75 / 108                   49
 // It depends on the shape alone, so the bits of a result do too.
 #include "fp8_plan.h"
 
@@ -25,7 +27,8 @@ constexpr int kMostRuns = 32;
 constexpr int64_t kPartBytes = 64 << 20;     // most bytes of partials
 // Workgroups stay within one grid of fewer than 2^32 threads.
 constexpr int64_t kMostGroups = (1 << 23) - 512;
-constexpr double kTraffic = 5.0e6;           // bytes per us
+constexpr double kTraffic = 5.0e6;           // bytes per us: written and read again
+constexpr double kStream = 5.6e6;            // read once
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -58,6 +61,7 @@ mok_status make_blk_matmul_plan(const mok_fp8_shape *s, BlkPlan *p) {
     if (M == 0) return MOK_OK;
     // the experts' rows are not known here: taken as equal
     const int64_t experts = s->E > 0 ? std::min<int64_t>(s->E, M) : 1, rows = ceil_div(M, experts);
+    const double stream = (double)experts * N * s->K / kStream;   // the weights' bytes
     double least = 1e30;
 
     // 128-row tiles, the contraction in runs
@@ -67,7 +71,8 @@ mok_status make_blk_matmul_plan(const mok_fp8_shape *s, BlkPlan *p) {
         if (ceil_div(kb, run) != r) continue;
         if (r > 1 && (r * M * N * 4 > kPartBytes || (ceil_div(M, 128) + s->E) * cols * r > kMostGroups)) break;
         const double step = (groups <= 192 ? 0.83 : 0.95) * (p->f32 ? 1.8 : 1.0);
-        const double us = 5.0 + (double)ceil_div(groups, kUnits) * (run * step + 1.0) + join_us(r, M * N);
+        const double us =
+            5.0 + std::max(stream, (double)ceil_div(groups, kUnits) * (run * step + 1.0)) + join_us(r, M * N);
         if (us < least) {
             least = us;
             p->splits = r;
@@ -83,8 +88,8 @@ mok_status make_blk_matmul_plan(const mok_fp8_shape *s, BlkPlan *p) {
             whole -= whole % kUnits;
         }
         half = std::max<int64_t>(half - (ceil_div(whole, kUnits) * kUnits - whole), 0);   // beside the last whole ones
-        const double us = 5.0 + (double)ceil_div(whole, kUnits) * (kb * 1.6 + 3.0) +
-                          (double)ceil_div(half, kUnits) * (kb * 0.95 + 1.0);
+        const double us = 5.0 + std::max(stream, (double)ceil_div(whole, kUnits) * (kb * 1.6 + 3.0) +
+                                                     (double)ceil_div(half, kUnits) * (kb * 0.95 + 1.0));
         if (us < least) {
             least = us;
             p->bm = 256;
@@ -94,10 +99,12 @@ mok_status make_blk_matmul_plan(const mok_fp8_shape *s, BlkPlan *p) {
     }
     // 16 rows of the weights a workgroup, 16 mt rows at a time
     if (experts * N / 16 <= (1 << 22)) {
-        constexpr double rate[3] = {4.6e6, 2.8e6, 1.6e6};   // bytes of weights per us
+        // a pass is the weights' bytes, or its own latency; all rows of X come from L2 to every workgroup
+        constexpr double rate[3] = {12e6, 9e6, 6.5e6};
         for (int i = 0; i < 3; ++i) {
             const int64_t passes = ceil_div(rows, 16 << i);
-            const double us = 3.0 + (double)passes * experts * N * s->K / rate[i];
+            const double us =
+                1.0 + (double)passes * std::max(stream, 2.5) + (double)M * (N / 16) * s->K / rate[i];
             if (us < least) {
                 least = us;
                 p->bm = 128;
