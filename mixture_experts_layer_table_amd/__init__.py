@@ -1247,7 +1247,9 @@ def fp8_quantize(src, src_is_k_by_rows: bool = False, tile: bool = False, glu: b
     if _elsewhere(dev):
         with torch.cuda.device(dev):
             return fp8_quantize(src, src_is_k_by_rows, tile, glu, outs)
-    elems, scales = (src.new_empty((B, rows, K), dtype=_U8), src.new_empty(sshape, dtype=_F32)) if outs is None else outs
+    if outs is None:
+        outs = src.new_empty((B, rows, K), dtype=_U8), src.new_empty(sshape, dtype=_F32)
+    elems, scales = outs
     flags = (MOK_FP8_TURNED if src_is_k_by_rows else 0) | (MOK_FP8_TILE if tile else 0) | (MOK_FP8_GLU if glu else 0)
     _check(_lib.mok_fp8_quantize(src.data_ptr(), sd, B, rows, K, flags, elems.data_ptr(), scales.data_ptr(),
                                  _raw_stream(dev.index)), "mok_fp8_quantize")

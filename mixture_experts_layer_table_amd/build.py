@@ -17,8 +17,8 @@ LIB = os.path.join(PKG, "libmok.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["plan.cpp", "ffn_plan.cpp", "timing.cpp", "streams.cpp", "schedule.hip", "layer.hip", "layer_mx.hip", "mxfp8.hip", "router.hip",
-           "dropout.hip", "norm.hip", "sort.hip", "rows.hip", "fp8_quant.hip", "fp8_plan.cpp", "fp8_matmul.hip", "fp8_few.hip",
-           "ffn.hip", "ffn_mx.hip", "ffn_few.hip", "api.hip", "noalloc.hip"]
+           "dropout.hip", "norm.hip", "sort.hip", "rows.hip", "fp8_quant.hip", "fp8_plan.cpp",
+           "fp8_matmul.hip", "fp8_few.hip", "ffn.hip", "ffn_mx.hip", "ffn_few.hip", "api.hip", "noalloc.hip"]
 COMMON = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950",
           # packed fp32 vector ops stay off (v_pk_*_f32 are not generated)
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

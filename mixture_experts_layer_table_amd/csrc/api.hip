@@ -551,7 +551,7 @@ mok_status mok_fp8_quantize(const void *src, int32_t dtype, int64_t batch, int64
         rows < 0 || rows >= lim || K < 0 || K >= lim || K % 16 || (turned && rows % 8))
         return MOK_ERROR_INVALID_VALUE;
     if (glu && (tile || dtype != MOK_STREAM_BF16)) return MOK_ERROR_INVALID_VALUE;
-    if (rows && K >= (int64_t(1) << 40) / rows) return MOK_ERROR_INVALID_VALUE;
+    if (rows && K > ((int64_t(1) << 40) - 1) / rows) return MOK_ERROR_INVALID_VALUE;
     if (batch * rows * K == 0) return MOK_OK;
     if (!dev_ok(src) || !dev_ok(elems) || !dev_ok(scales)) return MOK_ERROR_INVALID_VALUE;
     const size_t n = (size_t)batch * rows * K, kb = (size_t)(K + 127) / 128;
@@ -564,7 +564,7 @@ mok_status mok_fp8_quantize(const void *src, int32_t dtype, int64_t batch, int64
 }
 
 mok_status mok_glu_backward(const void *da, const void *h, int64_t T, int32_t I, void *dh, void *stream) {
-    if (T < 0 || T >= (int64_t(1) << 31) || I <= 0 || I % 8 || T > (int64_t(1) << 40) / I)
+    if (T < 0 || T >= (int64_t(1) << 31) || I <= 0 || I % 8 || T > ((int64_t(1) << 40) - 1) / I)
         return MOK_ERROR_INVALID_VALUE;
     if (T == 0) return MOK_OK;
     if (!dev_ok(da) || !dev_ok(h) || !dev_ok(dh)) return MOK_ERROR_INVALID_VALUE;
@@ -599,7 +599,8 @@ mok_status mok_fp8_matmul(const mok_fp8_shape *shape, void *workspace, size_t wo
     BlkPlan p;
     const mok_status s = make_blk_matmul_plan(shape, &p);
     if (s != MOK_OK) return s;
-    if ((p.total > 0 && !dev_ok(workspace)) || !dev_ok(b_elems) || !dev_ok(b_scales) || (p.E > 0 ? !dev_ok(offsets) : offsets != nullptr))
+    if ((p.total > 0 && !dev_ok(workspace)) || !dev_ok(b_elems) || !dev_ok(b_scales) ||
+        (p.E > 0 ? !dev_ok(offsets) : offsets != nullptr))
         return MOK_ERROR_INVALID_VALUE;
     if (p.M > 0 && (!dev_ok(a_elems) || !dev_ok(a_scales) || !dev_ok(out))) return MOK_ERROR_INVALID_VALUE;
     if (workspace_bytes < p.total) return MOK_ERROR_BUFFER_TOO_SMALL;

@@ -28,8 +28,8 @@ __device__ __forceinline__ f32x4_t few_product(const i32x8v_t &w, const i32x8v_t
     if constexpr (EXACT) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(w[2 * i], w[2 * i + 1]), as_bf16(x[2 * i], x[2 * i + 1]),
-                                                        t, 0, 0, 0);
+            t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(w[2 * i], w[2 * i + 1]),
+                                                        as_bf16(x[2 * i], x[2 * i + 1]), t, 0, 0, 0);
     } else {
         t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, t, 0, 0, 0, 0, 0, 0);
     }

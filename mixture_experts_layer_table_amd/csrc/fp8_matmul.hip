@@ -124,7 +124,8 @@ __device__ __forceinline__ void store_tile(const f32x16_t (&acc)[C::FM][C::FN], 
         const brsrc_t add = rows_rsrc(addend ? static_cast<const char *>(addend) + at_byte : static_cast<char *>(out),
                                       addend ? bytes : 0u);
         const int pr = el >> 4, pu = el & 15;   // a pass: 4 rows of 16 lanes, 4 columns each
-        const uint32_t v0 = pu * 4 < valid ? (uint32_t)(wm * C::WM + pr) * row_bytes + (uint32_t)pu * 4u * es : kOutOfRange;
+        const uint32_t v0 =
+            pu * 4 < valid ? (uint32_t)(wm * C::WM + pr) * row_bytes + (uint32_t)pu * 4u * es : kOutOfRange;
 #pragma unroll
         for (int fm = 0; fm < FM; ++fm) {
 #pragma unroll
@@ -172,8 +173,9 @@ __device__ __forceinline__ void store_tile(const f32x16_t (&acc)[C::FM][C::FN], 
                     u32x2v_t w;
                     w.x = pack_bf16x2(c[g4 * 4], c[g4 * 4 + 1]);
                     w.y = pack_bf16x2(c[g4 * 4 + 2], c[g4 * 4 + 3]);
+                    const uint32_t to = area + (uint32_t)row * 128u + ((u ^ (uint32_t)(row >> 1 & 7)) << 4);
                     *reinterpret_cast<__attribute__((address_space(3))) u32x2v_t *>(
-                        (uintptr_t)(area + (uint32_t)row * 128u + ((u ^ (uint32_t)(row >> 1 & 7)) << 4) + (uint32_t)half * 8u)) = w;
+                        (uintptr_t)(to + (uint32_t)half * 8u)) = w;
                 }
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
@@ -181,7 +183,8 @@ __device__ __forceinline__ void store_tile(const f32x16_t (&acc)[C::FM][C::FN], 
                 const f32x4_t y = get16(area + (uint32_t)r * 128u + (uint32_t)((pu ^ (r >> 1 & 7)) << 4));
                 const u32x4s_t w = {__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]),
                                     __float_as_uint(y[3])};
-                __builtin_amdgcn_raw_buffer_store_b128(w, dst, (int)(v0 + (uint32_t)(fm * 32 + p * 8) * row_bytes), 0, 2);
+                __builtin_amdgcn_raw_buffer_store_b128(w, dst, (int)(v0 + (uint32_t)(fm * 32 + p * 8) * row_bytes), 0,
+                                                       2);
             }
         }
     }
@@ -200,7 +203,8 @@ __device__ __forceinline__ float lane_of_16(float x) {
 // waits for the one before (16,384 x 4,096 x 7,168 of 4 experts: 488 against 469 us;
 // 412 with one scale a row).
 template <int R0, int... R>
-__device__ __forceinline__ void row_scales(float (&m)[sizeof...(R)], float s, float sw, std::integer_sequence<int, R...>) {
+__device__ __forceinline__ void row_scales(float (&m)[sizeof...(R)], float s, float sw,
+                                           std::integer_sequence<int, R...>) {
     ((m[R] = s * lane_of_16<R0 + R>(sw)), ...);
 }
 template <bool WROWS, int R0 = 0>
@@ -358,7 +362,8 @@ __device__ __forceinline__ void blk_tile(const BlkArgs &a, const BlkTile &t, uin
                 if constexpr (C::EARLY_W) {
 #pragma unroll
                     for (int i = 0; i < L; ++i)
-                        if (i <= XL ? fm == FM - 1 && fn == i / 3 : fm == 1 + (i - 1 - XL) / 4 && fn == (i - 1 - XL) / 2 % 2)
+                        if (i <= XL ? fm == FM - 1 && fn == i / 3
+                                    : fm == 1 + (i - 1 - XL) / 4 && fn == (i - 1 - XL) / 2 % 2)
                             issue(i, kt + S, st, scn);
                 } else if (fm == FM - 1) {
                     issue_with(fn, kt + S, st, scn);
@@ -535,8 +540,8 @@ int64_t most_row_tiles(const BlkArgs &a, int bm) { return ceil_div(a.M, bm) + (a
 unsigned rounded(int64_t workgroups) { return (unsigned)(ceil_div(workgroups, kXcds) * kXcds); }
 
 template <class K>
-hipError_t launch_tiles(K *kernel, const char *name, unsigned grid, int threads, size_t lds, std::atomic<uint64_t> &done,
-                        const BlkArgs &a, hipStream_t st) {
+hipError_t launch_tiles(K *kernel, const char *name, unsigned grid, int threads, size_t lds,
+                        std::atomic<uint64_t> &done, const BlkArgs &a, hipStream_t st) {
     const hipError_t e = allow_lds(kernel, lds, done);
     if (e != hipSuccess) return e;
     KernelTimer tm(name, st);

@@ -7,7 +7,10 @@
 // All four go by token: a token's row is read once and stays in registers
 // while its k rows are written (and quantized once, not k times), or its k rows
 // are read into one sum; no row is touched twice and nothing is added through
-// memory. Bound by HBM.
+// memory. Bound by HBM; 2,048 tokens of 7,168 bf16, 8 choices each: permute to 8-bit
+// rows 31 us (4.8 TB/s; its scales go out as single words), unpermute 55 us (5.3
+// TB/s); unpermute backward, 1,001 x 4,096 fp32, 2 choices, 17 us (3.9 TB/s: 66 MB,
+// of which a launch's start and end are a quarter).
 //
 // Rows that pad an expert's run get zeros from workgroups of their own in the
 // same launch. Slots are checked against the number of rows, so a damaged table
@@ -307,7 +310,8 @@ mok_status launch_unpermute_backward(const RowsCall &c, const void *dout, const 
     a.tokens_end = c.T;
     const int64_t groups = c.T + ceil_of(c.rows, kPadRows);
     const char *name = "unpermute_backward";
-    // one or two choices: two chunks each in flight; more: one chunk of eight
+    // Choices at once: two for k <= 2 (1,001 x 4,096 bf16, k = 1: 4.4 us against 5.9 with eight), else eight
+    // (1,001 x 4,096 fp32, k = 8: 59 against 62).
     hipError_t e;
     if (c.k <= 2)
         e = c.f32 ? launch_groups(unpermute_backward_kernel<kF32, 2, 2>, name, a, groups, st)

@@ -8,11 +8,14 @@
 // order, rounded up to `align` and scanned over the experts. Integers only, and
 // no atomics: the table is a pure function of the ids.
 //
-// Up to kSortFew slots and kSortFewE experts it is one launch: workgroups of 1,024
+// Below kSortFew slots and up to kSortFewE experts it is one launch: workgroups of 1,024
 // slots, each of which counts all slots for itself, those ahead of its own apart.
 // Sixteen of them read the same 64 KiB from L2, which is cheaper than a second
 // launch; what bounds it is the chain of barriers and dependent accesses. Past
 // that, three launches: a count per wave, a scan over the waves, and the placing.
+// One launch against three, us in a graph of calls: 8 slots 4.8 / 9.7, 16,384 slots
+// 8.0 / 32, 65,536 slots 17 / 33 (256 experts) and 20.7 / 25 (8 experts); at 131,072
+// slots they meet (29 / 34 and about 34 / 26).
 #include <algorithm>
 
 #include "common.h"
@@ -24,7 +27,7 @@ namespace {
 
 constexpr int kSortWaves = 16;
 constexpr int64_t kSortChunk = kSortWaves * 64;   // slots of a workgroup
-constexpr int64_t kSortFew = 32 * kSortChunk;
+constexpr int64_t kSortFew = 64 * kSortChunk;
 constexpr int kSortFewE = 512;                    // counters of 16 waves: 32 KiB of LDS
 constexpr int64_t kSortGroups = 1024;             // most waves of the three-launch form
 
@@ -77,7 +80,7 @@ __device__ __forceinline__ int round_up(int v, int align) { return (v + align - 
 
 __global__ __launch_bounds__(64 * kSortWaves) void sort_few(SortArgs a) {
     __shared__ int32_t count[kSortWaves][kSortFewE + 1];
-    __shared__ int32_t total[kSortFewE + 1], ahead[kSortFewE + 1];   // of all slots, and of those before this workgroup's
+    __shared__ int32_t ahead[kSortFewE + 1], total[kSortFewE + 1];   // slots before this workgroup's, and all others
     __shared__ int32_t first[kSortFewE + 1];
     __shared__ int32_t wave_sum[kSortWaves];
     const int tid = (int)threadIdx.x, wave = tid >> 6, lane = tid & 63;
@@ -203,7 +206,7 @@ bool sort_plan(int64_t T, int k, int E, int align, SortPlan *p) {
     if (n >= (int64_t(1) << 31) || rows >= (int64_t(1) << 31)) return false;
     p->n = n;
     p->rows = rows;
-    p->few = n <= kSortFew && E <= kSortFewE;
+    p->few = n < kSortFew && E <= kSortFewE;
     const int64_t waves = std::max<int64_t>(1, std::min(kSortGroups, (n + 1023) / 1024));
     p->chunk = p->few ? kSortChunk : std::max<int64_t>(64, (n + waves * 64 - 1) / (waves * 64) * 64);
     p->groups = (int)std::max<int64_t>(1, (n + p->chunk - 1) / p->chunk);

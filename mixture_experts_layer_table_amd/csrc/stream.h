@@ -22,8 +22,10 @@ __device__ __forceinline__ void stream8_elems(void *base, int64_t c, const float
     if constexpr (E == kBf16) {
         stream16(base, c, pack8_bf16(f));
     } else {
-        stream16(base, 2 * c, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
-        stream16(base, 2 * c + 1, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])));
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            stream16(base, 2 * c + i, make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]),
+                                                 __float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3])));
     }
 }
 template <Elem E>

@@ -8,10 +8,11 @@ import routed_reference as R
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 
-# one workgroup up to 16,384 slots and 512 experts, three launches past either
+# one launch below 65,536 slots and up to 512 experts, else three
 CASES = [(1, 1, 1, 1), (1, 8, 256, 1), (3, 2, 4, 128), (64, 1, 7, 16), (65, 3, 8, 1), (1023, 1, 512, 16),
          (2048, 8, 256, 128), (16384, 1, 4, 128), (2049, 8, 256, 16), (5000, 4, 8, 1024), (300, 8, 513, 3),
-         (1, 4, 4096, 1), (163840, 1, 8, 128), (20000, 2, 4096, 1)]
+         (1, 4, 4096, 1), (163840, 1, 8, 128), (20000, 2, 4096, 1),
+         (65535, 1, 8, 16), (65536, 1, 8, 16)]
 
 
 def _ids(T, k, E, kind):
