@@ -603,7 +603,7 @@ mok_status launch_fp8_matmul(const BlkPlan &p, void *workspace, const uint8_t *a
     a.splits = p.splits;
     a.run = p.run;
     hipError_t e;
-    if (p.few) e = launch_blk_few(a, p.few, p.f32, st);
+    if (p.few) e = launch_blk_few(a, p.few, p.few_w, p.f32, st);
     else if (p.bm == 256) e = launch_mixed(a, st);
     else e = p.f32 ? launch_matmul<CfgM, true>(a, st) : launch_matmul<CfgM, false>(a, st);
     if (e == hipSuccess && p.splits > 1) e = launch_join(a, p.f32, p.M * p.N, true, st);

@@ -8,11 +8,11 @@
 //   rows x N x K              few rows at 16 / 32 / 64   128-row tiles in 1 / 4 / 8 runs   256-row tiles
 //   1 x 4,096 x 7,168         7.7* / 8.7 / 11.2          44 / 19 / 14                      44
 //   32 x 4,096 x 7,168        16.3 / 12.7* / 16.3        44 / 20 / 15.5                    45
-//   64 x 7,168 x 2,048        18.7 / 15.3 / 13.4*        16.9 / 15.6 / 18.9                17.1
+//   64 x 7,168 x 2,048        19 / 11.9 / 10.1*          16.9 / 15.7 / 18.9                17.1
 //   64 x 4,096 x 7,168        33 / 27 / 26               44 / 20.7 / 17.3*                 45
 //   512 x 4,096 x 7,168       228 / 170 / 162            50 / 32* / 48                     51
 //   2,048 x 7,168 x 2,048     495 / 387 / 311            41 / 122 / 242                    33*
-//   16 of 16 experts, 7,168 x 2,048   45.5* / 54 / 82    47.7 / 75 / 108                   49
+//   16 of 16 experts, 7,168 x 2,048   42* / 40 / 61      47.8 / 75 / 108                   49
 // It depends on the shape alone, so the bits of a result do too.
 #include "fp8_plan.h"
 
@@ -99,8 +99,12 @@ mok_status make_blk_matmul_plan(const mok_fp8_shape *s, BlkPlan *p) {
     }
     // 16 rows of the weights a workgroup, 16 mt rows at a time
     if (experts * N / 16 <= (1 << 22)) {
+        // Two tiles of W a workgroup read X once for both and keep more loads in flight, where they still fill the
+        // card. us with one and two: 64 x 7,168 x 2,048 13.2 / 10.4, 32 rows 9.0 / 7.6, 16 experts of one row 46 / 42,
+        // of 8 rows 57 / 44; but 64 x 4,096 x 7,168 (128 workgroups) 24 / 30, one row 7.8 / 10.4.
+        const int w = experts * (N / 32) >= 192 ? 2 : 1;
         // a pass is the weights' bytes, or its own latency; all rows of X come from L2 to every workgroup
-        constexpr double rate[3] = {12e6, 9e6, 6.5e6};
+        const double rate[3] = {w == 2 ? 30e6 : 12e6, 9e6, 6.5e6};
         for (int i = 0; i < 3; ++i) {
             const int64_t passes = ceil_div(rows, 16 << i);
             const double us =
@@ -110,6 +114,7 @@ mok_status make_blk_matmul_plan(const mok_fp8_shape *s, BlkPlan *p) {
                 p->bm = 128;
                 p->splits = 1;
                 p->few = 1 << i;
+                p->few_w = w;
             }
         }
     }

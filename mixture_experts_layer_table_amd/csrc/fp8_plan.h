@@ -12,7 +12,7 @@ struct BlkPlan {
     int N, K, E;
     bool f32;
     int bm;            // tile rows
-    int few;           // tiles of 16 rows of the few-rows kernel; 0: not taken
+    int few, few_w;    // tiles of 16 rows, and of 16 weight rows, of the few-rows kernel; 0: not taken
     int splits, run;   // runs of the contraction, joined by a second kernel; K-blocks of one (products by weights)
     size_t total;      // workspace bytes (0: none)
 };

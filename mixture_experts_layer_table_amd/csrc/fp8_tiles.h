@@ -65,7 +65,8 @@ __device__ __forceinline__ Found find_tile(const BlkArgs &a, int i, F &&count) {
     return Found{-1, 0, 0, 0};   // i is not below the sum
 }
 
-// The product by weights for few rows (fp8_few.hip): mt tiles of 16 rows at a time (1, 2 or 4).
-hipError_t launch_blk_few(const BlkArgs &a, int mt, bool f32, hipStream_t st);
+// The product by weights for few rows (fp8_few.hip): mt tiles of 16 rows at a time (1, 2 or 4), nw tiles of 16 weight
+// rows a workgroup (1 or 2).
+hipError_t launch_blk_few(const BlkArgs &a, int mt, int nw, bool f32, hipStream_t st);
 
 }  // namespace mok

@@ -7,6 +7,11 @@ DENSE = {
     "few_2": (25, 4096, 2048, False, (2, 128, 1)),
     "few_4": (60, 1024, 1040, False, (4, 128, 1)),
     "few_4_two_passes": (100, 512, 272, False, (4, 128, 1)),
+    "few_1_wide": (16, 6160, 1040, False, (1, 128, 1)),
+    "few_2_wide": (25, 7184, 1040, False, (2, 128, 1)),              # 32 columns a workgroup, the last one 16
+    "few_4_wide": (60, 6160, 2048, False, (4, 128, 1)),
+    "few_4_wide_f32": (50, 7168, 1040, True, (4, 128, 1)),
+    "few_2_wide_f32": (30, 6160, 272, True, (2, 128, 1)),
     "few_f32": (20, 1024, 4096, True, (2, 128, 1)),
     "runs": (128, 2064, 7168, False, (0, 128, None)),
     "runs_short_last": (300, 1040, 7088, False, (0, 128, None)),
@@ -22,6 +27,8 @@ DENSE = {
 GROUPED = {
     "few": ([3, 0, 1, 7], 1024, 1040, False, (1, 128, 1)),
     "few_uneven": ([40, 0, 0, 2], 1024, 1040, False, (1, 128, 1)),   # three passes for one expert
+    "few_1_wide": ([2, 0, 1, 16, 20], 2064, 1040, True, (1, 128, 1)),
+    "few_wide": ([30, 0, 1, 40, 20], 2064, 1040, False, (2, 128, 1)),
     "runs": ([100, 0, 60, 30], 1040, 7168, False, (0, 128, None)),
     "tiles_128": ([130, 250, 0, 1, 380], 2064, 1040, False, (0, 128, 1)),
     "mixed": ([300, 0, 90, 1513, 256, 129, 2000, 512], 4096, 2048, False, (0, 256, 1)),

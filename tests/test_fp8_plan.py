@@ -19,7 +19,7 @@ class Shape(ctypes.Structure):
 
 class Plan(ctypes.Structure):
     _fields_ = [("bm", ctypes.c_int32), ("few", ctypes.c_int32), ("splits", ctypes.c_int32), ("run", ctypes.c_int32),
-                ("total", ctypes.c_size_t)]
+                ("total", ctypes.c_size_t), ("few_w", ctypes.c_int32)]
 
 
 @pytest.fixture(scope="module")
@@ -27,11 +27,11 @@ def plan(tmp_path_factory):
     d = tmp_path_factory.mktemp("plan")
     src, lib = d / "plan.cpp", d / "plan.so"
     src.write_text(f'''#include "{CSRC}/fp8_plan.h"
-struct Out {{ int32_t bm, few, splits, run; size_t total; }};
+struct Out {{ int32_t bm, few, splits, run; size_t total; int32_t few_w; }};
 extern "C" int plan(int wgrad, const mok_fp8_shape *s, Out *o) {{
     mok::BlkPlan p;
     const int r = wgrad ? mok::make_blk_wgrad_plan(s, &p) : mok::make_blk_matmul_plan(s, &p);
-    if (r == 0) *o = Out{{p.bm, p.few, p.splits, p.run, p.total}};
+    if (r == 0) *o = Out{{p.bm, p.few, p.splits, p.run, p.total, p.few_w}};
     return r;
 }}
 ''')
@@ -59,6 +59,13 @@ def test_grouped_shapes_take_their_path(plan, name):
     rows, N, K, f32, (few, bm, runs) = S.GROUPED[name]
     p = plan(False, sum(rows), N, K, len(rows), f32)
     assert (p.few, p.bm) == (few, bm) and (p.splits == runs if runs else p.splits > 1)
+
+
+def test_few_rows_take_both_widths(plan):
+    for shapes, grouped in ((S.DENSE, False), (S.GROUPED, True)):
+        for name, (rows, N, K, f32, (few, _, _)) in shapes.items():
+            p = plan(False, sum(rows) if grouped else rows, N, K, len(rows) if grouped else 0, f32)
+            assert p.few_w == (0 if few == 0 else 2 if "wide" in name else 1), name
 
 
 @pytest.mark.parametrize("name", list(S.WGRAD))
