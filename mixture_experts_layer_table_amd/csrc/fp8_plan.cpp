@@ -122,6 +122,13 @@ mok_status make_blk_matmul_plan(const mok_fp8_shape *s, BlkPlan *p) {
     return MOK_OK;
 }
 
+// Weight gradients, us (rows, N x K of each expert; the choice marked *):
+//                             256-row tiles   128-row tiles in 1 / 4 / 8 / 16 runs
+//   512, 4,096 x 7,168        31*             35 / 242 / 448
+//   8,192, 512 x 512          96              60 / 24 / 20.0 / 20.8 (13 runs: 20.6*)
+//   1,024, 2,048 x 2,048      18              13.2* / 35 / 59
+//   16,384 of 4, 2,048 x 1,024    57          43.7* / 95 / 149
+//   8,192 of 16, 7,168 x 2,048    198*        253
 mok_status make_blk_wgrad_plan(const mok_fp8_shape *s, BlkPlan *p) {
     if (!widths_ok(s) || s->M >= (int64_t(1) << 23) || s->M % 16) return MOK_ERROR_INVALID_VALUE;
     fill(s, p);
