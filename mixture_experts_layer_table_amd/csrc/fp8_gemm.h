@@ -65,10 +65,11 @@ struct BlkLoader {
     static __device__ __forceinline__ uint32_t lane_row(uint32_t ld) {
         return (uint32_t)(wave_id() * IPW * 8 + (int)((threadIdx.x & 63) >> 3)) * ld;
     }
-    // base: the tile's first row at the run's first byte; ld: bytes from row to row
+    // base: the tile's first row at the run's first byte; ld: bytes from row to row, a multiple of 16. A run's last
+    // chunk is loaded whole, in the last row too: past a shorter buffer's end nothing of it would come.
     __device__ __forceinline__ void init(const uint8_t *base, uint32_t ld, int nrows, int len_) {
         len = len_;
-        res = make_rsrc(base, nrows > 0 && len > 0 ? (uint32_t)(nrows - 1) * ld + (uint32_t)len : 0u);
+        res = make_rsrc(base, nrows > 0 && len > 0 ? (uint32_t)(nrows - 1) * ld + (((uint32_t)len + 15u) & ~15u) : 0u);
         ld8 = ld * 8;
         lds0 = (uint32_t)(wave_id() * IPW * 1024);
     }
@@ -81,6 +82,23 @@ struct BlkLoader {
                    tile + lds0 + (uint32_t)(i * 1024));
     }
 };
+
+// Zeros behind a run's end in the last 16-byte chunk of its last K-block, in every tile row (len: the run's, no
+// multiple of 16). Each lane clears one of the rows that its own wave loaded (X rows in the lower half of the wave, W
+// rows in the upper one), so the wave's own wait for its loads is enough before, and the workgroup's barrier after.
+template <class C>
+__device__ __forceinline__ void clear_behind(uint32_t tile, int len) {
+    constexpr int XR = BlkLoader<C, C::BM>::IPW * 8, WR = BlkLoader<C, C::BN>::IPW * 8;
+    static_assert(XR <= 32 && WR <= 32, "a row a lane");
+    const bool upper = threadIdx.x & 32;
+    const int i = threadIdx.x & 31, row = wave_id() * (upper ? WR : XR) + i, c = (len & (kBlk - 1)) / 16;
+    if (i < (upper ? WR : XR)) {
+        const uint32_t at = tile + (uint32_t)((upper ? C::X_BYTES : 0) + row * kBlk + (c ^ ((row >> 1) & 7)) * 16);
+        typedef __attribute__((address_space(3))) uint8_t lds_u8;
+        for (int b = len & 15; b < 16; ++b) *(lds_u8 *)(uintptr_t)(at + (uint32_t)b) = 0;
+    }
+    wait_lgkm0();
+}
 
 // MFMA operand of 32 tile rows for half s (64 values) of the K-block: lane l
 // holds row l % 32, chunks 4 s + 2 (l / 32) and the next one. (The order of k

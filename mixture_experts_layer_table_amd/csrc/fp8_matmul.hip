@@ -226,7 +226,11 @@ __device__ __forceinline__ void scaled_add(f32x16_t &acc, const f32x16_t &p, flo
 }
 
 // WROWS: W has a scale per row and block (weight gradients), else per 128 rows and
-// block. F32: fp32 results, whose products are exact (blk_product).
+// block. F32: fp32 results, whose products are exact (blk_product). CUT: the
+// contraction ends inside a 16-byte chunk, as an expert's run of rows may; what
+// lies behind it there belongs to no expert and may be NaN, so it is cleared in
+// LDS. By itself, because a branch in the loop costs 1 to 2% (16,384 x 4,096 x
+// 7,168 of 4 experts: 484 -> 497 us), code behind the loop 12% by its registers.
 //
 // A wave goes through its FM x FN block tiles of a K-block in row order, one
 // tile's MFMAs issued ahead of the previous tile's multiply-adds (two product
@@ -242,7 +246,7 @@ __device__ __forceinline__ void scaled_add(f32x16_t &acc, const f32x16_t &p, flo
 // turn, 401 with the loads in branchless form, 386 with three of a wave's nine loads
 // a tile instead of all behind the barrier, 371 with the second barrier; 282 without
 // loads and multiply-adds, where the clock (1.9 GHz) is the limit.
-template <class C, bool WROWS, bool F32>
+template <class C, bool WROWS, bool F32, bool CUT = false>
 __device__ __forceinline__ void blk_tile(const BlkArgs &a, const BlkTile &t, uint32_t lds) {
     constexpr int FM = C::FM, FN = C::FN, S = C::NSTAGE;
     static_assert(FN == 2 && FM >= 2, "two products in turn; fragments one row of tiles ahead");
@@ -328,6 +332,10 @@ __device__ __forceinline__ void blk_tile(const BlkArgs &a, const BlkTile &t, uin
             for (int fn = 0; fn < FN; ++fn) sw_rows[fn] = *((const lds_f32 *)(uintptr_t)b + fn * 32);
         }
     };
+    auto clear_last = [&] {
+        wait_vmcnt<0>();
+        clear_behind<C>(stage(nk - 1), t.len);
+    };
     // K-block kt
     auto block = [&](int kt) {
         uint32_t st = stage(kt), st1 = stage(kt + 1), sc = scales(kt), sc1 = scales(kt + 1);
@@ -378,6 +386,7 @@ __device__ __forceinline__ void blk_tile(const BlkArgs &a, const BlkTile &t, uin
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
+        if (CUT && kt == nk - 3) clear_last();   // all its loads are out, the barrier before its first read is to come
         read_sx(sc1);
     };
     // as if block -1 had come before
@@ -390,6 +399,7 @@ __device__ __forceinline__ void blk_tile(const BlkArgs &a, const BlkTile &t, uin
     for (int i = 0; i < EARLY; ++i) issue(i, S - 1, stage(S - 1), scales(S - 1));
     static_assert((L + C::PER_TILE - 1) / C::PER_TILE <= FM * FN, "a block's loads go out before the next barrier");
     wait_vmcnt<(S - 2) * L + EARLY>();
+    if (CUT && nk <= 2) clear_last();
     lds_barrier();
     read_sx(scales(0));
     x[0] = read_frag<0>(stage(0) + x_rows + frag);
@@ -487,7 +497,8 @@ __global__ __launch_bounds__(C::NT, 2) void blk_wgrad(BlkArgs a) {
     t.len = max(r1 - r0, 0);
     t.out = ((int64_t)e * a.M + m0) * a.N + n0;
     t.part = a.part + (int64_t)s * max(a.E, 1) * a.M * a.N;
-    blk_tile<C, true, F32>(a, t, lds_base());
+    if (t.len & 15) blk_tile<C, true, F32, true>(a, t, lds_base());
+    else blk_tile<C, true, F32>(a, t, lds_base());
 }
 
 // out = addend + sum of the runs' partials, in ascending order, 4 values a thread; 8 loads are in flight before the
