@@ -479,8 +479,9 @@ __global__ __launch_bounds__(C::NT, 2) void blk_wgrad(BlkArgs a) {
     const int m0 = mt * C::BM, n0 = col % gx * C::BN, s = col / gx;
     int r0 = 0, r1 = a.K;
     if (a.E > 0) {
-        r0 = uniform_i(clamp_row(a.offsets[e], a.K)) & ~(kBlk - 1);
-        r1 = uniform_i(clamp_row(a.offsets[e + 1], a.K));
+        const int lo = uniform_i(clamp_row(a.offsets[e], a.K)), hi = uniform_i(clamp_row(a.offsets[e + 1], a.K));
+        r0 = lo & ~(kBlk - 1);
+        r1 = lo < hi ? hi : r0;   // an expert without rows may lie where another's run ended, inside a block
     }
     if (a.splits > 1) {   // this expert's blocks in equal runs
         const int run = ((r1 - r0 + kBlk - 1) / kBlk + a.splits - 1) / a.splits * kBlk;

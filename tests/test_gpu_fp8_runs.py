@@ -69,3 +69,21 @@ def test_a_nan_code_inside_the_last_unit_stays():
     dy[0][10, end] = 0x7F
     nan = torch.isnan(mok.fp8_wgrad(dy, x, torch.tensor([0, end]).int().to(DEV), out_dtype=F32))
     assert nan[0, 9].all() and int(nan.sum()) == K
+
+
+@pytest.mark.parametrize("addend", [False, True])
+@pytest.mark.parametrize("name", PATHS)
+def test_an_expert_without_rows_where_another_run_ends(name, addend):
+    N, K, M, dtype = _case(name)
+    N, K = min(N, 512), min(K, 528)          # several experts' fit the reference; their path may be another
+    print(f"[runs] empty {name} {addend}", flush=True)
+    dy, x = row_codes(N, M, 9), row_codes(K, M, 10)
+    for ends in ([0, 0, 130, 130, 130, 130], [37, 37, 37, 37, 37], [128, 128, 256 + 16, 256 + 16], [M - 16, M - 16]):
+        off = torch.tensor(ends).int()
+        E = len(ends) - 1
+        add = torch.randn(E, N, K, device=DEV).to(dtype) if addend else None
+        got = mok.fp8_wgrad(dy, x, off.to(DEV), out_dtype=dtype, addend=add)
+        _check(got, *R.wgrad(R.row_values(*dy), R.row_values(*x), off, add), 256)
+        for e in range(E):
+            if ends[e] == ends[e + 1]:
+                assert torch.equal(got[e], add[e]) if addend else (got[e] == 0).all()
