@@ -684,7 +684,9 @@ mok_status mok_fp8_matmul(const mok_fp8_shape *shape, void *workspace, size_t wo
  * with MOK_FP8_TURNED, 128 rows a block). The runs start at multiples of 128 (a
  * sort with align = 128) and end at any row: the codes behind an end count for
  * nothing, whatever they are. (The scale of the block it lies in counts them, if
- * mok_fp8_quantize made it.) An expert without rows gets its addend, or zeros.
+ * mok_fp8_quantize made it.) A run that starts elsewhere gives NaN throughout: its
+ * first block's scales hold for another expert's rows too. An expert without rows
+ * gets its addend, or zeros, wherever its offset lies.
  *   dy_elems, dy_scales   device uint8 [N,M] and fp32 [(M+127)/128, N]
  *   x_elems, x_scales     device uint8 [K,M] and fp32 [(M+127)/128, K]
  *   addend                device out_dtype [E or 1, N, K], or NULL

@@ -1358,9 +1358,10 @@ def fp8_wgrad(dy, x, offsets=None, out_dtype=torch.bfloat16, addend=None, out=No
     dy: (elems uint8 [N, R], scales fp32 [ceil(R/128), N]), x: (elems uint8 [K, R],
     scales fp32 [ceil(R/128), K]), both from fp8_quantize(.., src_is_k_by_rows=True)
     of the R rows. ``offsets``: int32 [E + 1] whose runs start at multiples of 128
-    (sort_tokens with align=128) and end at any row, or None for one product.
-    Returns [E, N, K] or [N, K] in bf16 or fp32; ``addend`` and ``out`` have that
-    shape, and ``out`` may be addend. N, K and R are multiples of 16."""
+    (sort_tokens with align=128; one that starts elsewhere gives NaN) and end at
+    any row, or None for one product. Returns [E, N, K] or [N, K] in bf16 or fp32;
+    ``addend`` and ``out`` have that shape, and ``out`` may be addend. N, K and R
+    are multiples of 16."""
     el, sc, N, R = _row_codes(dy, "dy")
     dev = el.device
     xel, xsc, K, R2 = _row_codes(x, "x", dev)

@@ -17,6 +17,7 @@ struct BlkTile {
     const float *xs, *ws;    // scales of the first row (W by tiles: the first block row) at k0
     int rows, cols, len;
     int64_t out;             // first element in out (and in a run's partials)
+    bool refused;            // the result is NaN (CUT, see blk_tile)
     float *part;             // partials of the tile's run of the contraction
 };
 
@@ -229,8 +230,9 @@ __device__ __forceinline__ void scaled_add(f32x16_t &acc, const f32x16_t &p, flo
 // block. F32: fp32 results, whose products are exact (blk_product). CUT: the
 // contraction ends inside a 16-byte chunk, as an expert's run of rows may; what
 // lies behind it there belongs to no expert and may be NaN, so it is cleared in
-// LDS. By itself, because a branch in the loop costs 1 to 2% (16,384 x 4,096 x
-// 7,168 of 4 experts: 484 -> 497 us), code behind the loop 12% by its registers.
+// LDS; and a run that is refused gets its NaN here. By itself, because a branch in
+// the loop costs 1 to 2% (16,384 x 4,096 x 7,168 of 4 experts: 484 -> 497 us), code
+// behind the loop 12% by its registers.
 //
 // A wave goes through its FM x FN block tiles of a K-block in row order, one
 // tile's MFMAs issued ahead of the previous tile's multiply-adds (two product
@@ -399,7 +401,7 @@ __device__ __forceinline__ void blk_tile(const BlkArgs &a, const BlkTile &t, uin
     for (int i = 0; i < EARLY; ++i) issue(i, S - 1, stage(S - 1), scales(S - 1));
     static_assert((L + C::PER_TILE - 1) / C::PER_TILE <= FM * FN, "a block's loads go out before the next barrier");
     wait_vmcnt<(S - 2) * L + EARLY>();
-    if (CUT && nk <= 2) clear_last();
+    if (CUT && nk > 0 && nk <= 2) clear_last();
     lds_barrier();
     read_sx(scales(0));
     x[0] = read_frag<0>(stage(0) + x_rows + frag);
@@ -409,6 +411,15 @@ __device__ __forceinline__ void blk_tile(const BlkArgs &a, const BlkTile &t, uin
     join(FM - 1, FN - 1);
     wait_vmcnt<0>();   // the loads of blocks past the last, which write zeros
     lds_barrier();   // the waves' staging areas lie where blocks were
+    if constexpr (CUT) {
+        const float more = t.refused ? __builtin_nanf("") : 0.0f;
+#pragma unroll
+        for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+            for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[fm][fn][r] += more;
+    }
 
     if (a.splits > 1)   // fp32 partials, joined by a second kernel
         store_tile<C, true>(acc, t, a.N, t.part, nullptr, lds, wm, wn);
@@ -478,10 +489,14 @@ __global__ __launch_bounds__(C::NT, 2) void blk_wgrad(BlkArgs a) {
     group_tile(id, gy, cols, mt, col);
     const int m0 = mt * C::BM, n0 = col % gx * C::BN, s = col / gx;
     int r0 = 0, r1 = a.K;
+    bool refused = false;
     if (a.E > 0) {
         const int lo = uniform_i(clamp_row(a.offsets[e], a.K)), hi = uniform_i(clamp_row(a.offsets[e + 1], a.K));
         r0 = lo & ~(kBlk - 1);
         r1 = lo < hi ? hi : r0;   // an expert without rows may lie where another's run ended, inside a block
+        // Operands have one scale for a block's rows, whoever they belong to: no run begins inside one. Only the device
+        // knows the offsets, so the answer to one that does is NaN.
+        refused = r0 < lo && lo < hi;
     }
     if (a.splits > 1) {   // this expert's blocks in equal runs
         const int run = ((r1 - r0 + kBlk - 1) / kBlk + a.splits - 1) / a.splits * kBlk;
@@ -498,7 +513,8 @@ __global__ __launch_bounds__(C::NT, 2) void blk_wgrad(BlkArgs a) {
     t.len = max(r1 - r0, 0);
     t.out = ((int64_t)e * a.M + m0) * a.N + n0;
     t.part = a.part + (int64_t)s * max(a.E, 1) * a.M * a.N;
-    if (t.len & 15) blk_tile<C, true, F32, true>(a, t, lds_base());
+    t.refused = refused;
+    if (uniform_i((t.len & 15) | (int)refused)) blk_tile<C, true, F32, true>(a, t, lds_base());
     else blk_tile<C, true, F32>(a, t, lds_base());
 }
 

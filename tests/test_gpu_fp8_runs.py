@@ -87,3 +87,22 @@ def test_an_expert_without_rows_where_another_run_ends(name, addend):
         for e in range(E):
             if ends[e] == ends[e + 1]:
                 assert torch.equal(got[e], add[e]) if addend else (got[e] == 0).all()
+
+
+@pytest.mark.parametrize("addend", [False, True])
+@pytest.mark.parametrize("name", PATHS)
+def test_a_run_that_begins_inside_a_block_is_nan(name, addend):
+    N, K, M, dtype = _case(name)
+    N, K = min(N, 512), min(K, 528)
+    print(f"[runs] start {name} {addend}", flush=True)
+    dy, x = row_codes(N, M, 11), row_codes(K, M, 12)
+    ends = [0, 100, 256, 300, 301, 301, 384]
+    off, E = torch.tensor(ends).int(), len(ends) - 1
+    add = torch.randn(E, N, K, device=DEV).to(dtype) if addend else None
+    got = mok.fp8_wgrad(dy, x, off.to(DEV), out_dtype=dtype, addend=add)
+    ref, mag = R.wgrad(R.row_values(*dy), R.row_values(*x), off, add)
+    for e in range(E):
+        if ends[e] % 128 and ends[e + 1] > ends[e]:
+            assert torch.isnan(got[e]).all(), e
+        else:
+            _check(got[e], ref[e], mag[e], 128)
