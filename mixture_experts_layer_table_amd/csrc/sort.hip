@@ -76,7 +76,11 @@ __device__ __forceinline__ int wave_scan(int v) {   // inclusive
     return v;
 }
 
-__device__ __forceinline__ int round_up(int v, int align) { return (v + align - 1) / align * align; }
+// Unsigned: a sort near the limits has v + align - 1 past 2^31, the rounded value below it.
+__device__ __forceinline__ constexpr int round_up(int v, int align) {
+    return (int)(((uint32_t)v + (uint32_t)align - 1u) / (uint32_t)align * (uint32_t)align);
+}
+static_assert(round_up(2147483000, 1000) == 2147483000 && round_up(2147482001, 1000) == 2147483000, "no wrap");
 
 __global__ __launch_bounds__(64 * kSortWaves) void sort_few(SortArgs a) {
     __shared__ int32_t count[kSortWaves][kSortFewE + 1];
