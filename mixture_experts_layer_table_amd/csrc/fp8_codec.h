@@ -14,7 +14,7 @@ constexpr int kBlk = 128;
 
 struct BlkScale {
     float scale, mul;
-    uint32_t nan;   // ORed onto four codes
+    uint32_t nan;   // in place of four codes where it is not 0
 };
 // amax_bits: bits of the block's largest |fp32| (a NaN's lie above infinity's).
 __device__ __forceinline__ BlkScale blk_scale(uint32_t amax_bits) {
@@ -25,7 +25,8 @@ __device__ __forceinline__ BlkScale blk_scale(uint32_t amax_bits) {
 constexpr float kLeastScale = 0x1p-52f / 448.0f;   // of a block of zeros
 
 __device__ __forceinline__ uint32_t blk_codes4(const BlkScale &b, float v0, float v1, float v2, float v3) {
-    return b.nan | e4m3x2_scaled(v0 * b.mul, v1 * b.mul) | (e4m3x2_scaled(v2 * b.mul, v3 * b.mul) << 16);
+    const uint32_t q = e4m3x2_scaled(v0 * b.mul, v1 * b.mul) | (e4m3x2_scaled(v2 * b.mul, v3 * b.mul) << 16);
+    return b.nan ? b.nan : q;
 }
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }

@@ -133,3 +133,32 @@ def test_nothing_to_quantize():
         assert el.numel() == 0
     assert mok.glu_backward(torch.empty((0, 8), dtype=BF, device=DEV),
                             torch.empty((0, 16), dtype=BF, device=DEV)).shape == (0, 16)
+
+
+@pytest.mark.parametrize("what", [float("nan"), float("-inf")])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("form", ["rows", "tile", "turned", "turned tile", "gated", "gated turned", "permuted"])
+def test_codes_of_a_block_with_no_number_are_7f(form, dtype, what):
+    # values of both signs in a block that holds a NaN or an infinity
+    if form.startswith("gated") and dtype is not BF:
+        pytest.skip("gated sources are bf16")
+    v = _source(1, 128, 256, F32)
+    if form.startswith("gated"):
+        v = torch.cat([v.abs() + 1.0, v], 2)      # g > 0: silu(g) * u has u's sign
+        v[0, 17, 256 + 40] = what
+    else:
+        v[0, 17, 40] = what
+    v = v.to(dtype)
+    if form == "permuted":
+        ids = torch.zeros(128, 1, dtype=torch.int32, device=DEV)
+        el = mok.permute(v[0].contiguous(), mok.sort_tokens(ids, 1), rows=False, fp8=True)["elems"][None]
+    else:
+        turned = "turned" in form
+        src = v.transpose(1, 2).contiguous() if turned and "gated" not in form else v
+        if form == "gated turned":                # [K, 2 rows]: g of all rows, then u
+            src = torch.cat([v[:, :, :256].transpose(1, 2), v[:, :, 256:].transpose(1, 2)], 2).contiguous()
+        el, _ = mok.fp8_quantize(src, turned, tile="tile" in form, glu="gated" in form)
+    hit = torch.zeros(el.shape, dtype=torch.bool, device=DEV)
+    hit[0, slice(0, 128) if "tile" in form else 17, :128] = True
+    assert (el[hit] == 0x7F).all(), el[hit].unique().tolist()
+    assert ((el[~hit] & 0x7F) != 0x7F).all()
