@@ -531,8 +531,8 @@ typedef struct mok_sort_shape {
 } mok_sort_shape;
 
 /* Host-only: the most rows that a sort of this shape fills, and the workspace
-   bytes of mok_sort_tokens (0 up to some ten thousand slots: the workspace may
-   then be NULL). Either pointer may be NULL. T >= 0, k >= 1, 1 <= E <=
+   bytes of mok_sort_tokens (0 below 65,536 slots of at most 512 experts: the
+   workspace may then be NULL). Either pointer may be NULL. T >= 0, k >= 1, 1 <= E <=
    4096, 1 <= align <= 1024; T*k and the rows stay below 2^31. */
 mok_status mok_sort_tokens_size(const mok_sort_shape *shape, int64_t *rows, size_t *workspace_bytes);
 

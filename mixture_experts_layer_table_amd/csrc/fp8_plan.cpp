@@ -59,7 +59,9 @@ mok_status make_blk_matmul_plan(const mok_fp8_shape *s, BlkPlan *p) {
     const int64_t M = s->M, N = s->N, kb = ceil_div(s->K, 128), cols = ceil_div(N, 256);
     if ((ceil_div(M, 128) + s->E) * cols > kMostGroups) return MOK_ERROR_UNSUPPORTED;
     if (M == 0) return MOK_OK;
-    // the experts' rows are not known here: taken as equal
+    // The experts' rows are not known here: taken as equal. Rows on one expert alone read one expert's weights, fewer
+    // bytes in more passes: in us, equal / half of the rows on one / all on one, 16 experts x 8 rows x 7,168 x 2,048 (the
+    // few-rows kernel) 40 / 50 / 30, 64 x 64 rows (tiles) 203 / 208 / 83, 16 x 32 rows x 4,096 x 7,168 91 / 125 / 46.
     const int64_t experts = s->E > 0 ? std::min<int64_t>(s->E, M) : 1, rows = ceil_div(M, experts);
     const double stream = (double)experts * N * s->K / kStream;   // the weights' bytes
     double least = 1e30;
@@ -127,8 +129,10 @@ mok_status make_blk_matmul_plan(const mok_fp8_shape *s, BlkPlan *p) {
 //   512, 4,096 x 7,168        31*             35 / 242 / 448
 //   8,192, 512 x 512          96              60 / 24 / 20.0 / 20.8 (13 runs: 20.6*)
 //   1,024, 2,048 x 2,048      18              13.2* / 35 / 59
-//   16,384 of 4, 2,048 x 1,024    57          43.7* / 95 / 149
+//   16,384 of 4, 2,048 x 1,024    57          43.7 - 46* / 95 / 149
 //   8,192 of 16, 7,168 x 2,048    198*        253
+// All of these are far from their floors (12.4, 1.7, 3.2, 25.6 and 105 us): a tile's stages fill a compute unit's LDS,
+// so one workgroup runs on it and its fill, drain and store overlap with nothing.
 mok_status make_blk_wgrad_plan(const mok_fp8_shape *s, BlkPlan *p) {
     if (!widths_ok(s) || s->M >= (int64_t(1) << 23) || s->M % 16) return MOK_ERROR_INVALID_VALUE;
     fill(s, p);

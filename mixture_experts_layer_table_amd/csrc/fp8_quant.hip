@@ -10,9 +10,10 @@
 //           values of K x 128 rows, a thread 8 rows of 8 consecutive k, so that it
 //           packs 8 codes of a row at once; they pass through LDS and leave as
 //           whole 128-byte lines of their rows.
-// Measured: 4 x 4,096 x 7,168 bf16 turned in tiles 66 us (5.3 TB/s), 16,384 x 7,168
-// rows 62 us (5.7 TB/s), 2,047 x 2,048 gated rows 6.5 us (3.2 TB/s: 21 MB are a
-// short launch), the gated activation's gradient of 16,384 x 2,048 57 us (5.9 TB/s).
+// Measured: 4 x 4,096 x 7,168 bf16 in tiles 65 us (5.4 TB/s), turned 66 us; 16,384 x 7,168
+// rows 62 us (5.7 TB/s), turned 78 (4.6); 16,384 x 2,048 gated rows 33 us (5.2 TB/s), turned
+// 35; 2,047 x 2,048 gated rows 6.5 us alone (3.2 TB/s: 21 MB are a short launch); the
+// gated activation's gradient of 16,384 x 2,048 57 us (5.9 TB/s).
 // With GLU the source rows are [g | u] and v = silu(g) * u is quantized.
 #include "fp8_codec.h"
 #include "glu.h"

@@ -8,9 +8,10 @@
 // while its k rows are written (and quantized once, not k times), or its k rows
 // are read into one sum; no row is touched twice and nothing is added through
 // memory. Bound by HBM; 2,048 tokens of 7,168 bf16, 8 choices each: permute to 8-bit
-// rows 31 us (4.8 TB/s; its scales go out as single words), unpermute 55 us (5.3
-// TB/s); unpermute backward, 1,001 x 4,096 fp32, 2 choices, 17 us (3.9 TB/s: 66 MB,
-// of which a launch's start and end are a quarter).
+// rows 31 us (4.8 TB/s; its scales go out as single words), as they are 53 us (5.5
+// TB/s; of fp32 242 us, 2.4 TB/s), unpermute 55 us (5.3 TB/s). Unpermute backward,
+// 1,001 x 4,096 fp32, 2 choices: 15.4 us in a stream of calls (4.3 TB/s: 66 MB, of
+// which a launch's start and end are a quarter), 16.8 alone.
 //
 // Rows that pad an expert's run get zeros from workgroups of their own in the
 // same launch. Slots are checked against the number of rows, so a damaged table
