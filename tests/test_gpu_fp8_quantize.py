@@ -135,13 +135,14 @@ def test_nothing_to_quantize():
                             torch.empty((0, 16), dtype=BF, device=DEV)).shape == (0, 16)
 
 
+NAN_FORMS = [(f, d) for f in ("rows", "tile", "turned", "turned tile", "gated", "gated turned", "permuted") for d in (BF, F32)
+             if d is BF or not f.startswith("gated")]
+
+
 @pytest.mark.parametrize("what", [float("nan"), float("-inf")])
-@pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("form", ["rows", "tile", "turned", "turned tile", "gated", "gated turned", "permuted"])
+@pytest.mark.parametrize("form,dtype", NAN_FORMS)
 def test_codes_of_a_block_with_no_number_are_7f(form, dtype, what):
     # values of both signs in a block that holds a NaN or an infinity
-    if form.startswith("gated") and dtype is not BF:
-        pytest.skip("gated sources are bf16")
     v = _source(1, 128, 256, F32)
     if form.startswith("gated"):
         v = torch.cat([v.abs() + 1.0, v], 2)      # g > 0: silu(g) * u has u's sign
